@@ -235,6 +235,106 @@ int muon_step_static(int n, const int* rows, const int* cols,
                      const muon_coeff* coeffs, int n_steps, float eps, int compute,
                      hipStream_t stream);
 
+/* ------------------------------------------- linear layers and layer norm */
+
+/* What the stepped matrices are used for between two steps: the products of
+ * a linear layer y = x W^T in 8-bit floating point (forward, and dx = dy W
+ * with a transposed copy of the weights), the activation kept in 8 bits for
+ * the backward pass, the weight gradient from it, which is what muon_step
+ * takes, and the layer norm in front.  W is out_features x in_features, as the
+ * step has it.
+ *
+ * These calls follow the conventions above, with these additions: matrices
+ * are row-major with a row stride (ld..., in elements, >= the row length);
+ * base pointers are MUON_PTR_ALIGN-aligned (weight, bias, mean, rstd and the
+ * scales: 4 bytes), rows need not be; rows, tokens == 0 is allowed and means
+ * that there is nothing to compute (sums over no rows are zero).  Outputs must
+ * overlap neither each other nor an input, nor the workspace anything
+ * (MUON_ERR_INVALID_ARG); between the rows of a strided output nothing is
+ * written.  The stream must belong to the current device. */
+
+/* An 8-bit tensor: rows x cols values in OCP e4m3, row-major, each row padded
+ * with zero bytes to a multiple of 128 columns (the row stride in bytes).
+ * Each block of block_rows x 128 values (block_rows 1 or 128) has one scale
+ * 2^e, held as the byte e + 127; a row of scales is padded to a multiple of
+ * 4 bytes (the padding is not used).  A value is its e4m3 number times its
+ * block's scale.  The library writes e = the smallest integer >= -117 such
+ * that no finite value of the block exceeds 448 * 2^e in magnitude, and rounds
+ * x / 2^e to nearest even; infinities and NaN become NaN and do not affect
+ * the scale.  A power of two costs no precision, and every value is exact
+ * in bf16.  Scales made elsewhere must have bytes 10 to 247 (e from -117 to
+ * 120), and the padding columns must be zero. */
+typedef struct {
+  void* data;     /* device, muon_tensor8_bytes(rows, cols) bytes, 16-byte aligned */
+  void* scale;    /* device, muon_tensor8_scale_bytes(...) bytes, 4-byte aligned */
+  int rows, cols; /* rows >= 0, 1 <= cols <= MUON_MAX_COLS8 */
+  int block_rows; /* 1 or 128 */
+} muon_tensor8;
+
+#define MUON_MAX_COLS8 (1 << 22)
+#define MUON_MAX_NORM_COLS 16384 /* longest row of a layer norm */
+
+/* Bytes of an 8-bit tensor's values and scales.  0 for rows == 0 or invalid sizes. */
+size_t muon_tensor8_bytes(int rows, int cols);
+size_t muon_tensor8_scale_bytes(int rows, int cols, int block_rows);
+
+/* x (rows x cols, bf16 or fp32) as an 8-bit tensor, and with `transposed` (a
+ * cols x rows tensor with block_rows 128; NULL: none) its transposed copy with
+ * the same values and scales, which needs out->block_rows == 128.
+ * MUON_ERR_UNSUPPORTED for a transposed copy of 1-row blocks. */
+int muon_quantize8(const void* x, int x_dtype, int rows, int cols, long long ldx,
+                   const muon_tensor8* out, const muon_tensor8* transposed, hipStream_t stream);
+
+/* The values of an 8-bit tensor as bf16 or fp32 (exact in both). */
+int muon_dequantize8(const muon_tensor8* t, void* y, int y_dtype, long long ldy,
+                     hipStream_t stream);
+
+/* y = a b^T for a (m x k) and b (n x k), y m x n in bf16 or fp32, sums in
+ * fp32.  Either operand may have either kind of block. */
+int muon_matmul8(const muon_tensor8* a, const muon_tensor8* b, void* y, int y_dtype,
+                 long long ldy, hipStream_t stream);
+
+/* dw = dy^T x, or with accumulate dw += dy^T x: the gradient of W (n x k,
+ * dense, as muon_step takes it) from the layer's output gradient dy (tokens x
+ * n, bf16; fp32 returns MUON_ERR_UNSUPPORTED) and its input x (tokens x k) kept
+ * in 8 bits.  Sums in fp32.  dw is fp32 or bf16; accumulating into bf16
+ * returns MUON_ERR_UNSUPPORTED (every addition would be rounded to 8 bits of
+ * mantissa).  The workspace (muon_weight_grad_workspace_bytes, possibly 0, then
+ * it may be NULL) holds partial sums. */
+size_t muon_weight_grad_workspace_bytes(int tokens, int n, int k);
+int muon_weight_grad(const void* dy, int dy_dtype, long long lddy, int tokens, int n,
+                     const muon_tensor8* x, void* dw, int dw_dtype, int accumulate,
+                     void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Layer norm over the columns of x (rows x cols, bf16 or fp32; cols up to
+ * MUON_MAX_NORM_COLS, more returns MUON_ERR_UNSUPPORTED):
+ *   mean = sum(x) / cols, rstd = 1 / sqrt(sum((x - mean)^2) / cols + eps),
+ *   y = (x - mean) * rstd * weight + bias
+ * weight, bias: fp32, cols elements; bias NULL: zero.  The output goes to y
+ * (bf16 or fp32) or, with y NULL, to the 8-bit tensor y8 (rows x cols,
+ * block_rows 1), rounded once from fp32; exactly one of the two is given.
+ * mean, rstd: fp32, rows elements, written for the backward pass. */
+int muon_layer_norm(const void* x, int x_dtype, long long ldx, int rows, int cols,
+                    const float* weight, const float* bias, float eps, void* y, int y_dtype,
+                    long long ldy, const muon_tensor8* y8, float* mean, float* rstd,
+                    hipStream_t stream);
+
+/* Its backward pass.  With xh = (x - mean) * rstd and g = dy * weight:
+ *   dx = rstd * (g - sum(g) / cols - xh * sum(g xh) / cols)
+ *   dweight = sum over rows of dy * xh,  dbias = sum over rows of dy
+ * x: the forward pass's input, bf16 or fp32, or with x NULL the 8-bit tensor x8
+ * that was kept of it (rows x cols); exactly one of the two.  dy and dx: bf16 or
+ * fp32, the same type.  dweight, dbias: fp32, cols elements, added to with
+ * accumulate; dbias may be NULL.  workspace:
+ * muon_layer_norm_backward_workspace_bytes, MUON_WORKSPACE_ALIGN-aligned. */
+size_t muon_layer_norm_backward_workspace_bytes(int rows, int cols);
+int muon_layer_norm_backward(const void* dy, int dy_dtype, long long lddy, const void* x,
+                             int x_dtype, long long ldx, const muon_tensor8* x8, int rows,
+                             int cols, const float* weight, const float* mean,
+                             const float* rstd, void* dx, long long lddx, float* dweight,
+                             float* dbias, int accumulate, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+
 /* ------------------------------------------------------------ measurement */
 
 /* Kernel classes reported by the timing log. */
@@ -247,7 +347,12 @@ typedef enum {
   MUON_K_FINAL = 5,  /* last step's a X + B X, written to the weights or output */
   MUON_K_NORMUON = 6, /* NorMuon row statistics and second-moment update */
   MUON_K_APPLY = 7,  /* weight update as its own pass (after NorMuon) */
-  MUON_K_GRAMQ = 8   /* one of the two launches forming A as Q A Q, Q = aI + B */
+  MUON_K_GRAMQ = 8,  /* one of the two launches forming A as Q A Q, Q = aI + B */
+  MUON_K_QUANT8 = 9, /* to or from an 8-bit tensor */
+  MUON_K_MATMUL8 = 10,
+  MUON_K_WEIGHT_GRAD = 11,
+  MUON_K_LAYER_NORM = 12,     /* forward */
+  MUON_K_LAYER_NORM_BACK = 13 /* backward, with the reduction of its sums */
 } muon_kernel_kind;
 
 typedef struct {

@@ -9,6 +9,14 @@ which PyTorch-ROCm exposes as ``torch.cuda.current_stream().cuda_stream``).
     step(params, grads, bufs, mu=, lr=, scales=, coeffs=)   in place
     step_ex(..., weight_decay=, cautious=, second_moments=, beta2=, normuon_eps=)
     step_static(params, grads, bufs, ...)          step with no workspace (fixed scratch)
+
+and, for the linear layers those matrices belong to (``layers.py``):
+
+    quantize8(x), dequantize8(t)                   8-bit tensors (Tensor8)
+    matmul8(a, b)                                  a b^T of two 8-bit tensors
+    weight_grad(dy, x8)                            dy^T x from the 8-bit activation
+    layer_norm(x, weight, bias)                    y, mean, rstd
+    layer_norm_backward(dy, x, weight, mean, rstd) dx, dweight, dbias
 """
 from __future__ import annotations
 
@@ -18,6 +26,7 @@ from . import _lib
 from ._lib import (  # noqa: F401
     EXPORTS, KERNEL_KINDS, MUON_BF16, MUON_FP32, MUON_MAX_STEPS, MUON_OK, MUON_ERR_HIP,
     MUON_ERR_INVALID_ARG, MUON_ERR_UNSUPPORTED, MUON_ERR_WORKSPACE, MUON_STATIC_SCRATCH_BYTES,
+    MUON_MAX_COLS8, MUON_MAX_NORM_COLS,
 )
 
 DEFAULT_EPS = 1e-7
@@ -357,3 +366,9 @@ def timing_read(cap: int = 1 << 16):
     return [dict(kind=KERNEL_KINDS[r.kind], m=r.m, n=r.n, batch=r.batch, step=r.step,
                  ms=r.ms, flops=r.flops, bytes=r.bytes, exec_flops=r.exec_flops)
             for r in arr[:n.value]]
+
+
+from .layers import (  # noqa: E402,F401
+    Tensor8, dequantize8, layer_norm, layer_norm_backward, layer_norm_backward_workspace_bytes,
+    matmul8, quantize8, weight_grad, weight_grad_workspace_bytes,
+)

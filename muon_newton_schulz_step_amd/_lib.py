@@ -13,8 +13,10 @@ MUON_MAX_STEPS = 64
 MUON_WORKSPACE_ALIGN = 256
 MUON_PTR_ALIGN = 16
 MUON_STATIC_SCRATCH_BYTES = 256 << 20
+MUON_MAX_COLS8 = 1 << 22
+MUON_MAX_NORM_COLS = 16384
 KERNEL_KINDS = ("prep", "norm", "gram", "poly", "update", "final", "normuon", "apply",
-                "gramq")
+                "gramq", "quant8", "matmul8", "weight_grad", "layer_norm", "layer_norm_back")
 
 # Every symbol include/muon.h declares.
 EXPORTS = (
@@ -31,6 +33,16 @@ EXPORTS = (
     "muon_timing_read",
     "muon_probe_mfma_bf16",
     "muon_probe_copy",
+    "muon_tensor8_bytes",
+    "muon_tensor8_scale_bytes",
+    "muon_quantize8",
+    "muon_dequantize8",
+    "muon_matmul8",
+    "muon_weight_grad_workspace_bytes",
+    "muon_weight_grad",
+    "muon_layer_norm",
+    "muon_layer_norm_backward_workspace_bytes",
+    "muon_layer_norm_backward",
 )
 
 
@@ -49,6 +61,11 @@ class MuonTimingRecord(ctypes.Structure):
                 ("batch", ctypes.c_int), ("step", ctypes.c_int), ("ms", ctypes.c_float),
                 ("flops", ctypes.c_double), ("bytes", ctypes.c_double),
                 ("exec_flops", ctypes.c_double)]
+
+
+class MuonTensor8(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("rows", ctypes.c_int), ("cols", ctypes.c_int), ("block_rows", ctypes.c_int)]
 
 
 _c_int_p = ctypes.POINTER(ctypes.c_int)
@@ -111,6 +128,22 @@ def load() -> ctypes.CDLL:
     lib.muon_timing_enable.restype = ctypes.c_int
     lib.muon_timing_read.argtypes = [ctypes.POINTER(MuonTimingRecord), ctypes.c_int, _c_int_p]
     lib.muon_timing_read.restype = ctypes.c_int
+    i, ll, sz, t8 = ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t, ctypes.POINTER(MuonTensor8)
+    for name, restype, argtypes in (
+            ("muon_tensor8_bytes", sz, [i, i]),
+            ("muon_tensor8_scale_bytes", sz, [i, i, i]),
+            ("muon_quantize8", i, [_vp, i, i, i, ll, t8, t8, _vp]),
+            ("muon_dequantize8", i, [t8, _vp, i, ll, _vp]),
+            ("muon_matmul8", i, [t8, t8, _vp, i, ll, _vp]),
+            ("muon_weight_grad_workspace_bytes", sz, [i, i, i]),
+            ("muon_weight_grad", i, [_vp, i, ll, i, i, t8, _vp, i, i, _vp, sz, _vp]),
+            ("muon_layer_norm", i, [_vp, i, ll, i, i, _vp, _vp, ctypes.c_float, _vp, i, ll, t8,
+                                    _vp, _vp, _vp]),
+            ("muon_layer_norm_backward_workspace_bytes", sz, [i, i]),
+            ("muon_layer_norm_backward", i, [_vp, i, ll, _vp, i, ll, t8, i, i, _vp, _vp, _vp, _vp,
+                                             ll, _vp, _vp, i, _vp, sz, _vp])):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = restype, argtypes
     _lib = lib
     return lib
 

@@ -1,0 +1,312 @@
+// Layer norm over the last axis, forward and backward.
+//   forward   mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps),
+//             y = (x - mu) r w + b, mu and r kept for the backward pass
+//   backward  xh = (x - mu) r, g = dy w:
+//             dx = r (g - mean(g) - xh mean(g xh)),
+//             dw = sum over rows of dy xh, db = sum over rows of dy
+// All sums are fp32.  Both passes read each row once and are bound by HBM.
+//
+// A team of TEAM waves holds a row in registers, 8 consecutive columns per
+// lane and chunk (a chunk: 512 columns per wave), so the mean and the sum of
+// squared deviations are two passes over registers, not over memory.  Teams
+// stay for many rows: the weights, and in the backward pass the columns'
+// gradient sums, are in registers all along.
+#include "fp8_device.h"
+#include "muon_layer.h"
+
+namespace muon {
+
+constexpr int kOut8 = 2;  // the 8-bit type among MUON_BF16, MUON_FP32
+
+template <int K> struct ElemOf { using type = float; };
+template <> struct ElemOf<MUON_BF16> { using type = bf16_t; };
+template <> struct ElemOf<kOut8> { using type = unsigned char; };
+
+// Sum over the team's waves of each wave's v, the same in all lanes.  `buf`
+// alternates between calls, so one barrier per call is enough.
+template <int TEAM, int N>
+__device__ __forceinline__ void team_sum(float (&v)[N], float (*buf)[16], int wave, int lane) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  if constexpr (TEAM > 1) {
+    if (lane == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) buf[i][wave] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float s = 0.f;
+#pragma unroll
+      for (int w = 0; w < TEAM; ++w) s += buf[i][w];
+      v[i] = s;
+    }
+  }
+}
+
+template <int XT, int OUT, int TEAM, int NCH>
+__global__ __launch_bounds__(TEAM > 4 ? 64 * TEAM : 256) void layer_norm_kernel(NormArgs a) {
+  using X = typename ElemOf<XT>::type;
+  using Y = typename ElemOf<OUT>::type;
+  constexpr int WAVES = TEAM > 4 ? TEAM : 4, TEAMS = WAVES / TEAM;
+  __shared__ float sums[2][1][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int tw = wave % TEAM;
+  const long long step = (long long)gridDim.x * TEAMS;
+  int col[NCH];
+  float w[NCH][8], b[NCH][8];
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) {
+    col[k] = ((k * TEAM + tw) * 64 + lane) * 8;
+    load8_edge(a.weight + col[k], a.cols - col[k], w[k]);
+    load8_edge(a.bias ? a.bias + col[k] : nullptr, a.bias ? a.cols - col[k] : 0, b[k]);
+  }
+  const float n = (float)a.cols;
+  for (long long row = (long long)blockIdx.x * TEAMS + wave / TEAM; row < a.rows; row += step) {
+    float x[NCH][8];
+    const X* xr = static_cast<const X*>(a.x) + row * a.ldx;
+    float s[1] = {0.f};
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      load8_edge(xr + col[k], a.cols - col[k], x[k]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[0] += x[k][i];
+    }
+    team_sum<TEAM>(s, sums[0], tw, lane);
+    const float mu = s[0] / n;  // exact for a row of equal values
+    s[0] = 0.f;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[k][i] = col[k] + i < a.cols ? x[k][i] - mu : 0.f;
+        s[0] = fmaf(x[k][i], x[k][i], s[0]);
+      }
+    team_sum<TEAM>(s, sums[1], tw, lane);
+    const float r = 1.f / sqrtf(s[0] / n + a.eps);
+    if (tw == 0 && lane == 0) {
+      a.mean[row] = mu;
+      a.rstd[row] = r;
+    }
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = fmaf(x[k][i] * r, w[k][i], b[k][i]);
+      if constexpr (OUT == kOut8) {
+        unsigned top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (col[k] + i >= a.cols) y[i] = 0.f;
+          const unsigned f = finite_bits(y[i]);
+          top = top > f ? top : f;
+        }
+        const int byte = scale_byte(max16(top));
+        const float inv = inv_scale_of(byte);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = inf_to_nan(y[i]) * inv;
+        if (col[k] < a.ld) *reinterpret_cast<u32x2_t*>(a.y8 + row * a.ld + col[k]) = to_e4m3(y);
+        const unsigned word = pack_scales(byte);
+        const int piece = k * TEAM + tw;
+        if (lane == 0 && 4 * piece < a.sld)
+          *reinterpret_cast<unsigned*>(a.s8 + row * a.sld + 4 * piece) = word;
+      } else {
+        store8_edge(static_cast<Y*>(a.y) + row * a.ldy + col[k], a.cols - col[k], y);
+      }
+    }
+  }
+}
+
+template <int DT, int XT, int TEAM, int NCH>
+__global__ __launch_bounds__(TEAM > 4 ? 64 * TEAM : 256) void layer_norm_back_kernel(
+    NormBackArgs a) {
+  using D = typename ElemOf<DT>::type;
+  using X = typename ElemOf<XT>::type;
+  constexpr int WAVES = TEAM > 4 ? TEAM : 4, TEAMS = WAVES / TEAM;
+  __shared__ float sums[2][2][16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int tw = wave % TEAM;
+  const long long step = (long long)gridDim.x * TEAMS;
+  int col[NCH];
+  float w[NCH][8], dw[NCH][8], db[NCH][8];
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) {
+    col[k] = ((k * TEAM + tw) * 64 + lane) * 8;
+    load8_edge(a.weight + col[k], a.cols - col[k], w[k]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[k][i] = db[k][i] = 0.f;
+  }
+  const float n = (float)a.cols;
+  int turn = 0;
+  for (long long row = (long long)blockIdx.x * TEAMS + wave / TEAM; row < a.rows; row += step) {
+    float x[NCH][8], d[NCH][8];
+    const float mu = a.mean[row], r = a.rstd[row];
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      if constexpr (XT == kOut8) {
+        u32x2_t q = {0u, 0u};
+        int byte = 127;
+        if (col[k] < a.ld) {
+          q = *reinterpret_cast<const u32x2_t*>(a.x8 + row * a.ld + col[k]);
+          byte = a.sx8[(row >> a.shift) * a.sld + (col[k] >> 7)];
+        }
+        from_e4m3(q, scale_of(byte), x[k]);
+      } else {
+        load8_edge(static_cast<const X*>(a.x) + row * a.ldx + col[k], a.cols - col[k], x[k]);
+      }
+      load8_edge(static_cast<const D*>(a.dy) + row * a.lddy + col[k], a.cols - col[k], d[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < NCH; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        // beyond the last column dy and w are zero, and x has no part
+        const float xh = col[k] + i < a.cols ? (x[k][i] - mu) * r : 0.f;
+        db[k][i] += d[k][i];
+        dw[k][i] = fmaf(d[k][i], xh, dw[k][i]);
+        const float g = d[k][i] * w[k][i];
+        s[0] += g;
+        s[1] = fmaf(g, xh, s[1]);
+        x[k][i] = xh;
+        d[k][i] = g;
+      }
+    team_sum<TEAM>(s, sums[turn], tw, lane);
+    turn ^= 1;
+    const float c0 = s[0] / n, c1 = s[1] / n;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = r * (d[k][i] - c0 - x[k][i] * c1);
+      store8_edge(static_cast<D*>(a.dx) + row * a.lddx + col[k], a.cols - col[k], o);
+    }
+  }
+  // the workgroup's sums: its teams' one after the other, in their order
+  float* part = a.part + (long long)blockIdx.x * 2 * a.cols;
+  if constexpr (TEAMS > 1) {
+    __shared__ float acc[2][NCH * 512];
+    for (int t = 0; t < TEAMS; ++t) {
+      if (wave == t)
+#pragma unroll
+        for (int k = 0; k < NCH; ++k)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int c = col[k] + i;
+            acc[0][c] = t ? acc[0][c] + dw[k][i] : dw[k][i];
+            acc[1][c] = t ? acc[1][c] + db[k][i] : db[k][i];
+          }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < a.cols; c += 64 * WAVES) {
+      part[c] = acc[0][c];
+      part[a.cols + c] = acc[1][c];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      store8_edge(part + col[k], a.cols - col[k], dw[k]);
+      store8_edge(part + a.cols + col[k], a.cols - col[k], db[k]);
+    }
+  }
+}
+
+// dw and db from the workgroups' partial sums, in their order: 64 columns
+// per workgroup, 16 waves over the partial rows, joined in LDS.
+__global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* part, int groups, int cols,
+                                                           float* dw, float* db, int accumulate) {
+  __shared__ float acc[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
+  float* out = blockIdx.y ? db : dw;
+  const float* p = part + (blockIdx.y ? cols : 0) + c;
+  float s = 0.f;
+  if (c < cols)
+#pragma unroll 8
+    for (int g = wave; g < groups; g += 16) s += p[(long long)g * 2 * cols];
+  acc[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < cols) {
+    s = 0.f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) s += acc[w][lane];
+    out[c] = accumulate ? out[c] + s : s;
+  }
+}
+
+namespace {
+// Team and chunks for a row of `cols` columns: one wave up to 2048, four up to
+// 8192, sixteen up to 16384; the fewest chunks that hold the row.
+template <typename F>
+void with_shape(int cols, F&& f) {
+  auto go = [&](auto team, auto nch) { f(team, nch); };
+#define MUON_SHAPE(T, N) go(std::integral_constant<int, T>{}, std::integral_constant<int, N>{})
+  if (cols <= 512) MUON_SHAPE(1, 1);
+  else if (cols <= 1024) MUON_SHAPE(1, 2);
+  else if (cols <= 1536) MUON_SHAPE(1, 3);
+  else if (cols <= 2048) MUON_SHAPE(1, 4);
+  else if (cols <= 4096) MUON_SHAPE(4, 2);
+  else if (cols <= 6144) MUON_SHAPE(4, 3);
+  else if (cols <= 8192) MUON_SHAPE(4, 4);
+  else MUON_SHAPE(16, 2);
+#undef MUON_SHAPE
+}
+int rows_per_group(int cols) { return cols <= 2048 ? 4 : 1; }
+int groups_for(int rows, int cols, int most) {
+  const int per = rows_per_group(cols);
+  const long long g = ((long long)rows + per - 1) / per;
+  return (int)(g < most ? g : most);
+}
+}  // namespace
+
+// Workgroups of the backward pass, each with one partial sum.
+int norm_backward_groups(int rows, int cols) { return groups_for(rows, cols, 512); }
+
+hipError_t launch_layer_norm(int x_bf16, int out, const NormArgs& a, hipStream_t s) {
+  with_shape(a.cols, [&](auto team, auto nch) {
+    constexpr int T = decltype(team)::value, N = decltype(nch)::value;
+    const dim3 grid(groups_for(a.rows, a.cols, T > 4 ? 512 : 2048)), block(T > 4 ? 64 * T : 256);
+    if (x_bf16) {
+      if (out == MUON_BF16)
+        hipLaunchKernelGGL((layer_norm_kernel<MUON_BF16, MUON_BF16, T, N>), grid, block, 0, s, a);
+      else if (out == MUON_FP32)
+        hipLaunchKernelGGL((layer_norm_kernel<MUON_BF16, MUON_FP32, T, N>), grid, block, 0, s, a);
+      else
+        hipLaunchKernelGGL((layer_norm_kernel<MUON_BF16, kOut8, T, N>), grid, block, 0, s, a);
+    } else {
+      if (out == MUON_BF16)
+        hipLaunchKernelGGL((layer_norm_kernel<MUON_FP32, MUON_BF16, T, N>), grid, block, 0, s, a);
+      else if (out == MUON_FP32)
+        hipLaunchKernelGGL((layer_norm_kernel<MUON_FP32, MUON_FP32, T, N>), grid, block, 0, s, a);
+      else
+        hipLaunchKernelGGL((layer_norm_kernel<MUON_FP32, kOut8, T, N>), grid, block, 0, s, a);
+    }
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_layer_norm_backward(int dy_bf16, int x, const NormBackArgs& a, hipStream_t s) {
+  if (a.groups > 0) with_shape(a.cols, [&](auto team, auto nch) {
+    constexpr int T = decltype(team)::value, N = decltype(nch)::value;
+    const dim3 grid(a.groups), block(T > 4 ? 64 * T : 256);
+    auto go = [&](auto dt) {
+      constexpr int D = decltype(dt)::value;
+      if (x == MUON_BF16)
+        hipLaunchKernelGGL((layer_norm_back_kernel<D, MUON_BF16, T, N>), grid, block, 0, s, a);
+      else if (x == MUON_FP32)
+        hipLaunchKernelGGL((layer_norm_back_kernel<D, MUON_FP32, T, N>), grid, block, 0, s, a);
+      else
+        hipLaunchKernelGGL((layer_norm_back_kernel<D, kOut8, T, N>), grid, block, 0, s, a);
+    };
+    if (dy_bf16)
+      go(std::integral_constant<int, MUON_BF16>{});
+    else
+      go(std::integral_constant<int, MUON_FP32>{});
+  });
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  hipLaunchKernelGGL(norm_reduce_kernel, dim3((a.cols + 63) / 64, a.dbias ? 2 : 1), dim3(1024), 0,
+                     s, a.part, a.groups, a.cols, a.dweight, a.dbias, a.accumulate);
+  return hipGetLastError();
+}
+
+}  // namespace muon

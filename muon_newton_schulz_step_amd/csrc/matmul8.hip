@@ -1,0 +1,352 @@
+// y = a b^T of two 8-bit tensors (e4m3, a power-of-two scale per block of 128
+// along the sum):
+//   y[m][n] = sum_k a[m][k] b[n][k],  a = qa 2^ea(m, k / 128), b likewise.
+// A bf16 result of many rows comes from v_mfma_scale_f32_32x32x64_f8f6f4, which
+// multiplies by both scales inside the instruction, so that the block scales
+// cost no vector work: a lane hands over the scale byte of its own row next to
+// its operand.  The instruction adds products in groups of 8 consecutive k in
+// fixed point, 13 bits below the group's largest exponent, the rest cut off
+// (measured: one product of 2^16 and one of m 2^(16 - j) in a group come out with
+// m cut to 13 - j fraction bits, and 0 from j = 14 on; the groups' sums and the
+// accumulator keep all 24 bits).  A result is thus off by less than
+// 7 * 2^-13 * sum of the groups' largest products; on Gaussian operands of any
+// length by 1.5e-5 of the result's norm, 1/110 of what rounding it to bf16 does
+// (1.7e-3).  A result in fp32 keeps more than that, so it comes from bf16 MFMAs
+// at half the rate, to whose operands the values are converted exactly
+// (EXACT; 1e-7 of the norm).
+//
+// Two kernels:
+//   tiles   both operands through LDS, for many rows of a: bound by the MFMAs;
+//   rows    few rows of a (up to kFewRows): bound by reading b once, so always
+//           exact.
+#include "muon_gemm.h"
+
+#include "fp8_device.h"
+#include "muon_layer.h"
+
+namespace muon {
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ i32x8_t frag8(const u32x4_t& lo, const u32x4_t& hi) {
+  return i32x8_t{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
+                 (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+// ---------------------------------------------------------------- tiles
+// A workgroup computes BN columns n (the MFMA's rows, operand b) by BM rows m
+// (its columns, operand a) of y.  k advances by one block of 128 per k-tile:
+// 128-byte operand rows of 8 chunks in LDS (swz), BN rows of b, then BM of a,
+// loaded straight into LDS, two stages.  A substep is 64 k, one 32x32x64
+// MFMA or (EXACT) four 32x32x16: lane (r, h) = (lane % 32, lane / 32) reads
+// chunks 4 kk + 2 h and the one after it of its row, for both operands the
+// same, so the order of k does not matter.  Rows past the last one read the last one
+// again and are not stored.
+template <int BM, int BN, int WGM, int WGN, bool EXACT, typename Y>
+__global__ __launch_bounds__(64 * WGM * WGN) void matmul8_tile_kernel(Matmul8Args g) {
+  constexpr int NW = WGM * WGN;
+  constexpr int WTM = BM / WGM, WTN = BN / WGN;
+  constexpr int FM = WTM / 32, FN = WTN / 32;
+  constexpr int CPR = 8;
+  constexpr int B_CHUNKS = BN * CPR, STAGE = (BM + BN) * CPR;
+  constexpr int DPW = STAGE / 64 / NW;
+  static_assert(DPW * 64 * NW == STAGE && B_CHUNKS % (DPW * 64) == 0, "one operand per wave");
+  // the epilogue's staging: 32 rows m of half the wave's columns, per wave
+  static_assert(FN % 2 == 0 && NW * 32 * (WTN / 2) * 4 <= STAGE * 16, "staging fits");
+  __shared__ u32x4_t S0[STAGE], S1[STAGE];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave / WGN, wn = wave % WGN;
+  const int L = xcd_remap((int)blockIdx.x, (int)gridDim.x);
+  const int span = g.group_m * g.tiles_n;
+  const int grp = L / span, first = grp * g.group_m;
+  const int gm = g.tiles_m - first < g.group_m ? g.tiles_m - first : g.group_m;
+  const int idx = L - grp * span;
+  const int m0 = (first + idx % gm) * BM, n0 = (idx / gm) * BN;
+
+  const int wave_s = __builtin_amdgcn_readfirstlane(wave);
+  const bool is_b = wave_s * DPW * 64 < B_CHUNKS;
+  const unsigned char* base = is_b ? g.b + (long long)n0 * g.ld : g.a + (long long)m0 * g.ld;
+  const int last_row = is_b ? g.n - 1 - n0 : g.m - 1 - m0;
+  unsigned voff[DPW];
+#pragma unroll
+  for (int d = 0; d < DPW; ++d) {
+    const int q = (wave * DPW + d) * 64 + lane;
+    const int r = q / CPR, rl = is_b ? r : r - BN;
+    voff[d] = (unsigned)(rl < last_row ? rl : last_row) * (unsigned)g.ld + swz(q % CPR, r) * 16;
+  }
+  auto issue = [&](int kt, u32x4_t* St) {
+    const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(base + (long long)kt * 128);
+#pragma unroll
+    for (int d = 0; d < DPW; ++d) buffer_load_lds16(rs, voff[d], St + (wave_s * DPW + d) * 64);
+  };
+
+  // scales of the lane's rows: a word holds those of four k-tiles
+  const unsigned* ps[FN + FM];
+  unsigned sc[FN + FM], sc_next[FN + FM];
+#pragma unroll
+  for (int f = 0; f < FN; ++f) {
+    const int r = n0 + wn * WTN + f * 32 + (lane & 31);
+    ps[f] = reinterpret_cast<const unsigned*>(
+        g.sb + (long long)((r < g.n ? r : g.n - 1) >> g.shift_b) * g.sld);
+  }
+#pragma unroll
+  for (int f = 0; f < FM; ++f) {
+    const int r = m0 + wm * WTM + f * 32 + (lane & 31);
+    ps[FN + f] = reinterpret_cast<const unsigned*>(
+        g.sa + (long long)((r < g.m ? r : g.m - 1) >> g.shift_a) * g.sld);
+  }
+  const int nk = g.ld / 128, last_word = (nk - 1) / 4;
+
+  f32x16_t acc[FN][FM];
+#pragma unroll
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
+
+  const int brow = wn * WTN + (lane & 31), arow = BN + wm * WTM + (lane & 31);
+  const int hsel = lane >> 5;
+  i32x8_t fb[2][FN], fa[2][FM];
+  auto fload = [&](const u32x4_t* St, int kk, int slot) {
+    const int ch = 4 * kk + 2 * hsel;
+#pragma unroll
+    for (int f = 0; f < FN; ++f) {
+      const int r = brow + f * 32;
+      fb[slot][f] = frag8(St[r * CPR + swz(ch, r)], St[r * CPR + swz(ch + 1, r)]);
+    }
+#pragma unroll
+    for (int f = 0; f < FM; ++f) {
+      const int r = arow + f * 32;
+      fa[slot][f] = frag8(St[r * CPR + swz(ch, r)], St[r * CPR + swz(ch + 1, r)]);
+    }
+  };
+  auto mfmas = [&](int slot) {
+    if constexpr (EXACT) {
+      float sf[FN + FM];
+#pragma unroll
+      for (int f = 0; f < FN + FM; ++f) sf[f] = scale_of((int)(sc[f] & 0xffu));
+#pragma unroll
+      for (int e = 0; e < 8; e += 2) {
+        u32x4_t wb[FN], wa[FM];
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+          wb[i] = bf16_of_e4m3((unsigned)fb[slot][i][e], (unsigned)fb[slot][i][e + 1], sf[i]);
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+          wa[j] = bf16_of_e4m3((unsigned)fa[slot][j][e], (unsigned)fa[slot][j][e + 1], sf[FN + j]);
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+          for (int j = 0; j < FM; ++j) mma<bf16_t>(acc[i][j], wb[i], wa[j]);
+      }
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+      for (int j = 0; j < FM; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            fb[slot][i], fa[slot][j], acc[i][j], 0, 0, 0, (int)sc[i], 0, (int)sc[FN + j]);
+  };
+  // The waves meet once the second substep's operands are in registers; the
+  // k-tile after next then goes into the stage just finished.
+  auto ktile = [&](int kt, u32x4_t* cur, const u32x4_t* nxt) {
+    fload(cur, 1, 1);
+    mfmas(0);
+    wait_vm_lgkm0();
+    barrier_no_fence();
+    issue(kt + 2 < nk ? kt + 2 : nk - 1, cur);
+    fload(nxt, 0, 0);
+    mfmas(1);
+    if ((kt & 3) == 3) {
+      const int word = (kt >> 2) + 2;
+#pragma unroll
+      for (int f = 0; f < FN + FM; ++f) {
+        sc[f] = sc_next[f];
+        sc_next[f] = ps[f][word < last_word ? word : last_word];
+      }
+    } else {
+#pragma unroll
+      for (int f = 0; f < FN + FM; ++f) sc[f] >>= 8;
+    }
+  };
+  issue(0, S0);
+#pragma unroll
+  for (int f = 0; f < FN + FM; ++f) {
+    sc[f] = ps[f][0];
+    sc_next[f] = ps[f][last_word < 1 ? last_word : 1];
+  }
+  wait_vmcnt<0>();
+  barrier_no_fence();
+  issue(nk > 1 ? 1 : 0, S1);
+  fload(S0, 0, 0);
+  for (int kt = 0; kt < nk; kt += 2) {
+    ktile(kt, S0, S1);
+    if (kt + 1 < nk) ktile(kt + 1, S1, S0);
+  }
+  wait_vmcnt<0>();
+  __syncthreads();
+
+  // Epilogue: acc holds, per lane, one row m and 4 consecutive columns n per
+  // register quad.  Each wave stages 32 rows m of half its columns as fp32 in
+  // its own part of the LDS (16-byte units, exchanged by row) and stores runs
+  // of 8 columns, neighbouring lanes neighbouring runs.
+  constexpr int HC = WTN / 2, UPR = HC / 4, RPR = HC / 8;  // units, runs per staged row
+  float* T = reinterpret_cast<float*>(S0) + wave * 32 * HC;
+  auto unit = [](int r, int u) __attribute__((always_inline)) {
+    return 4 * (r * UPR + (u ^ (r & (UPR - 1))));
+  };
+  Y* y = static_cast<Y*>(g.y);
+#pragma unroll
+  for (int j = 0; j < FM; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < FN / 2; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const f32x16_t& c = acc[h * (FN / 2) + i][j];
+          *reinterpret_cast<f32x4_t*>(T + unit(lane & 31, 8 * i + 2 * q + hsel)) =
+              f32x4_t{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
+        }
+      // only this wave touches its part, and a wave's LDS accesses execute in
+      // order: a compiler barrier orders them
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int s = 0; s < 32 * RPR / 64; ++s) {
+        const int t = lane + 64 * s, rr = t / RPR, c = t % RPR;
+        float v[8];
+        const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(T + unit(rr, 2 * c));
+        const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(T + unit(rr, 2 * c + 1));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = lo[e];
+          v[4 + e] = hi[e];
+        }
+        const int m = m0 + wm * WTM + j * 32 + rr, n = n0 + wn * WTN + h * HC + 8 * c;
+        if (m < g.m) store8_edge(y + (long long)m * g.ldy + n, g.n - n, v);
+      }
+      asm volatile("" ::: "memory");
+    }
+}
+
+// ---------------------------------------------------------------- rows
+// Up to 16 MF rows m.  A workgroup takes 16 columns n and its 8 waves share the
+// blocks of k between them; operands come straight from memory (each row of b
+// is used once) and go to bf16 in registers: four v_mfma_f32_16x16x32_bf16 per
+// block and 16 rows.  The waves' sums are added in their order through LDS.
+constexpr int kFewRows = 64, kFewWaves = 8;
+
+template <int MF, typename Y>
+__global__ __launch_bounds__(64 * kFewWaves) void matmul8_rows_kernel(Matmul8Args g) {
+  __shared__ f32x4_t sums[kFewWaves][MF][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int n0 = (int)blockIdx.x * 16;
+  const int r = lane & 15, grp = lane >> 4;
+  const int nb = g.ld / 128;
+  const int n = n0 + r < g.n ? n0 + r : g.n - 1;
+  const unsigned char* pb = g.b + (long long)n * g.ld + grp * 16;
+  const unsigned char* psb = g.sb + (long long)(n >> g.shift_b) * g.sld;
+  const unsigned char* pa[MF];
+  const unsigned char* psa[MF];
+  f32x4_t acc[MF];
+#pragma unroll
+  for (int f = 0; f < MF; ++f) {
+    const int m = 16 * f + r < g.m ? 16 * f + r : g.m - 1;
+    pa[f] = g.a + (long long)m * g.ld + grp * 16;
+    psa[f] = g.sa + (long long)(m >> g.shift_a) * g.sld;
+    acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  }
+  // chunks grp and grp + 4 of the block's eight: each load of a wave takes 64
+  // consecutive bytes of 16 rows
+  struct Frag {
+    u32x4_t lo, hi;
+    float scale;
+  };
+  auto load = [](const unsigned char* p, const unsigned char* s, int kb)
+                  __attribute__((always_inline)) {
+    return Frag{*reinterpret_cast<const u32x4_t*>(p + kb * 128),
+                *reinterpret_cast<const u32x4_t*>(p + kb * 128 + 64), scale_of(s[kb])};
+  };
+  auto bf16 = [](const Frag& f, int e) __attribute__((always_inline)) {
+    const u32x4_t& c = e < 2 ? f.lo : f.hi;
+    return __builtin_bit_cast(bf16x8_t,
+                              bf16_of_e4m3(c[2 * (e & 1)], c[2 * (e & 1) + 1], f.scale));
+  };
+  for (int kb = wave; kb < nb; kb += kFewWaves) {
+    const Frag fb = load(pb, psb, kb);
+    Frag fa[MF];
+#pragma unroll
+    for (int f = 0; f < MF; ++f) fa[f] = load(pa[f], psa[f], kb);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bf16x8_t wb = bf16(fb, e);
+#pragma unroll
+      for (int f = 0; f < MF; ++f)
+        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, bf16(fa[f], e), acc[f], 0, 0, 0);
+    }
+  }
+#pragma unroll
+  for (int f = 0; f < MF; ++f) sums[wave][f][lane] = acc[f];
+  __syncthreads();
+  // acc[f]: row m = 16 f + lane % 16, columns n0 + 4 (lane / 16) + 0 .. 3
+  for (int f = wave; f < MF; f += kFewWaves) {
+    f32x4_t s = sums[0][f][lane];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) s += sums[w][f][lane];
+    const int m = 16 * f + r, c = n0 + 4 * grp;
+    if (m < g.m) {
+      Y* y = static_cast<Y*>(g.y) + (long long)m * g.ldy + c;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (c + e < g.n) y[e] = from_f32<Y>(s[e]);
+    }
+  }
+}
+
+namespace {
+template <typename Y>
+void go(const Matmul8Args& in, hipStream_t s) {
+  Matmul8Args a = in;
+  if (a.m <= kFewRows) {
+    const dim3 grid((a.n + 15) / 16), block(64 * kFewWaves);
+    if (a.m <= 16)
+      hipLaunchKernelGGL((matmul8_rows_kernel<1, Y>), grid, block, 0, s, a);
+    else if (a.m <= 32)
+      hipLaunchKernelGGL((matmul8_rows_kernel<2, Y>), grid, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((matmul8_rows_kernel<4, Y>), grid, block, 0, s, a);
+    return;
+  }
+  auto tiles = [&](int bm, int bn) {
+    a.tiles_m = (a.m + bm - 1) / bm;
+    a.tiles_n = (a.n + bn - 1) / bn;
+    a.group_m = 8;
+    return (long long)a.tiles_m * a.tiles_n;
+  };
+  if constexpr (std::is_same_v<Y, float>) {
+    tiles(128, 128);
+    hipLaunchKernelGGL((matmul8_tile_kernel<128, 128, 2, 2, true, Y>),
+                       dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(256), 0, s, a);
+  } else if (tiles(256, 256) >= 256) {
+    hipLaunchKernelGGL((matmul8_tile_kernel<256, 256, 4, 2, false, Y>),
+                       dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(512), 0, s, a);
+  } else {
+    tiles(128, 128);
+    hipLaunchKernelGGL((matmul8_tile_kernel<128, 128, 2, 2, false, Y>),
+                       dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(256), 0, s, a);
+  }
+}
+}  // namespace
+
+hipError_t launch_matmul8(int y_bf16, const Matmul8Args& a, hipStream_t s) {
+  if (y_bf16)
+    go<bf16_t>(a, s);
+  else
+    go<float>(a, s);
+  return hipGetLastError();
+}
+
+}  // namespace muon

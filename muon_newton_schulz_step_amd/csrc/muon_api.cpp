@@ -19,8 +19,26 @@
 
 #include "muon.h"
 #include "muon_kernels.h"
+#include "muon_layer.h"
 
 using namespace muon;
+
+namespace muon {
+// The stream lanes of a concurrent step and the allocation-free entry
+// point's scratch belong to the calling thread's current device, and a layer
+// operator launches on it, so both refuse a stream of another device (MUON_ERR_INVALID_ARG, nothing
+// enqueued).  A handle the runtime cannot attribute to a device (the null
+// stream, special handles) passes; a bad one fails at its first launch.
+int check_stream_device(hipStream_t stream) {
+  int cur = -1;
+  if (hipGetDevice(&cur) != hipSuccess) return MUON_ERR_HIP;
+  hipDevice_t own = -1;
+  if (stream != nullptr && hipStreamGetDevice(stream, &own) == hipSuccess && own != cur)
+    return MUON_ERR_INVALID_ARG;
+  return MUON_OK;
+}
+
+}  // namespace muon
 
 namespace {
 
@@ -620,20 +638,6 @@ Lanes* lanes_of_current_device() {
   return &L;
 }
 
-// The stream lanes of a concurrent step and the allocation-free entry
-// point's scratch belong to the calling thread's current device, so a step
-// refuses a stream of another device (MUON_ERR_INVALID_ARG, nothing
-// enqueued).  A handle the runtime cannot attribute to a device (the null
-// stream, special handles) passes; a bad one fails at its first launch.
-int check_stream_device(hipStream_t stream) {
-  int cur = -1;
-  if (hipGetDevice(&cur) != hipSuccess) return MUON_ERR_HIP;
-  hipDevice_t own = -1;
-  if (stream != nullptr && hipStreamGetDevice(stream, &own) == hipSuccess && own != cur)
-    return MUON_ERR_INVALID_ARG;
-  return MUON_OK;
-}
-
 int check_options(const muon_options* o) {
   if (!o) return MUON_OK;
   if (!is_finite(o->weight_decay) || o->weight_decay < 0.f) return MUON_ERR_INVALID_ARG;
@@ -815,6 +819,11 @@ int step_impl(int n, const int* rows, const int* cols, void* const* params, int 
 }  // namespace
 
 namespace muon {
+hipError_t timed_call(int kind, int m, int n, double flops, double exec_flops, double bytes,
+                      hipStream_t s, hipError_t (*launch)(void*), void* arg) {
+  return timed(kind, m, n, 1, -1, flops, exec_flops, bytes, s, [&] { return launch(arg); });
+}
+
 int step_with_source(int n, const int* rows, const int* cols, void* const* params,
                      int param_dtype, const void* const* grads, int grad_dtype,
                      float* const* momentum, float mu, float lr, const float* scale,

@@ -1,0 +1,275 @@
+"""Linear layers in 8 bits and layer norm: what the stepped matrices are used
+for between two Muon steps.  Argument marshalling only, as in the package's
+``__init__``: every computation is a HIP kernel behind ``include/muon.h``.
+
+One linear layer y = x W^T behind a layer norm, forward and backward, and the
+step of its weights:
+
+    h8, mean, rstd = layer_norm(x, g, b, out_dtype=torch.float8_e4m3fn)
+    w8, w8t = quantize8(W, block_rows=128, transposed=True)   # once per step
+    y = matmul8(h8, w8)
+    ...                                                       # dy
+    dh = matmul8(quantize8(dy), w8t)
+    dx, dg, db = layer_norm_backward(dh, x, g, mean, rstd)
+    dW = weight_grad(dy, h8)                 # or out=dW, accumulate=True
+    step([W], [dW], [buf], mu=0.95, lr=0.02)
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import _lib
+from . import (MUON_BF16, MUON_FP32, MUON_OK, MuonError, _check_device, _dtype_code, _stream,
+               _torch, _workspace, lib)
+
+
+def _ld8(cols: int) -> int:
+    return -(-cols // 128) * 128
+
+
+def _scale_ld8(cols: int) -> int:
+    return -(-cols // 512) * 4
+
+
+class Tensor8:
+    """A matrix in 8 bits: e4m3 values and a power-of-two scale for each block
+    of ``block_rows`` x 128 (1 or 128 rows).
+
+    data   (rows, ld) torch.float8_e4m3fn, ld = cols rounded up to 128, the
+           padding columns zero
+    scale  (ceil(rows / block_rows), ceil(cols / 512) * 4) torch.uint8: the
+           byte e + 127 of the scale 2^e
+
+    A value is its e4m3 number times its block's scale."""
+
+    __slots__ = ("data", "scale", "cols", "block_rows", "_c")
+
+    def __init__(self, data, scale, cols: int, block_rows: int = 1):
+        torch = _torch()
+        if block_rows not in (1, 128):
+            raise ValueError("block_rows must be 1 or 128")
+        if not 1 <= cols <= _lib.MUON_MAX_COLS8:
+            raise ValueError(f"cols must lie in [1, {_lib.MUON_MAX_COLS8}]")
+        if data.dtype != torch.float8_e4m3fn or scale.dtype != torch.uint8:
+            raise TypeError("data must be float8_e4m3fn and scale uint8")
+        if data.dim() != 2 or data.shape[1] != _ld8(cols) or not data.is_contiguous():
+            raise ValueError("data must be contiguous, (rows, cols rounded up to 128)")
+        rows = data.shape[0]
+        if (scale.dim() != 2 or scale.shape[1] != _scale_ld8(cols) or not scale.is_contiguous()
+                or scale.shape[0] != -(-rows // block_rows)):
+            raise ValueError("scale must be contiguous, (blocks of rows, 4 ceil(cols / 512))")
+        if data.device != scale.device:
+            raise ValueError("data and scale must be on one device")
+        self.data, self.scale, self.cols, self.block_rows = data, scale, cols, block_rows
+        self._c = _lib.MuonTensor8(data.data_ptr(), scale.data_ptr(), rows, cols, block_rows)
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, block_rows: int = 1, device=None):
+        torch = _torch()
+        return cls(torch.empty((rows, _ld8(cols)), dtype=torch.float8_e4m3fn, device=device),
+                   torch.empty((-(-rows // block_rows), _scale_ld8(cols)), dtype=torch.uint8,
+                               device=device), cols, block_rows)
+
+    @property
+    def rows(self) -> int:
+        return self.data.shape[0]
+
+    @property
+    def shape(self):
+        return (self.data.shape[0], self.cols)
+
+    @property
+    def device(self):
+        return self.data.device
+
+    def dequantize(self, dtype=None):
+        return dequantize8(self, dtype)
+
+    def __repr__(self):
+        return f"Tensor8({self.rows} x {self.cols}, blocks of {self.block_rows} x 128)"
+
+
+def _matrix(t, name: str):
+    """(pointer, row stride) of a 2-D GPU tensor whose rows are dense."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = t.shape
+    if cols < 1:
+        raise ValueError(f"{name} must have at least one column")
+    ld, inner = t.stride()
+    if (inner != 1 and cols > 1) or (ld < cols and rows > 1):
+        raise ValueError(f"{name}: elements of a row must be adjacent, and rows not overlap")
+    return t.data_ptr(), ld if rows > 1 else cols
+
+
+def _vector(t, n: int, name: str):
+    if t.dtype != _torch().float32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous fp32 vector of {n} elements")
+    return t.data_ptr()
+
+
+def _call(device, name, *args):
+    torch = _torch()
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, _stream(device))
+    if st != MUON_OK:
+        raise MuonError(st, name)
+
+
+def quantize8(x, block_rows: int = 1, *, transposed: bool = False, out=None):
+    """``x`` (rows, cols), bf16 or fp32, as a Tensor8.  With ``transposed``
+    (128-row blocks only) returns (Tensor8 of x, Tensor8 of x^T): the same
+    values and scales in both layouts, in one pass."""
+    xp, ldx = _matrix(x, "x")
+    rows, cols = x.shape
+    code = _dtype_code(x.dtype)
+    if out is None:
+        out = Tensor8.empty(rows, cols, block_rows, x.device)
+    elif out.shape != (rows, cols) or out.block_rows != block_rows:
+        raise ValueError("out must be a Tensor8 of x's shape and block_rows")
+    _check_device(x.device, out=[out.data])
+    if transposed and block_rows != 128:
+        raise ValueError("a transposed copy needs block_rows=128")
+    if transposed and rows == 0:
+        raise ValueError("a tensor without rows has no transposed copy")
+    other = Tensor8.empty(cols, rows, 128, x.device) if transposed else None
+    _call(x.device, "muon_quantize8", xp, code, rows, cols, ldx, out._c,
+          other._c if transposed else None)
+    return (out, other) if transposed else out
+
+
+def dequantize8(t, dtype=None):
+    """The values of a Tensor8 as bf16 (default) or fp32, exact in both."""
+    torch = _torch()
+    dtype = dtype or torch.bfloat16
+    code = _dtype_code(dtype)
+    _check_device(t.device)
+    y = torch.empty((t.rows, t.cols), dtype=dtype, device=t.device)
+    _call(t.device, "muon_dequantize8", t._c, y.data_ptr(), code, t.cols)
+    return y
+
+
+def matmul8(a, b, *, out_dtype=None, out=None):
+    """a b^T of two Tensor8, (m, k) and (n, k) -> (m, n) in bf16 (default) or
+    fp32, sums in fp32.  ``out`` may have a row stride."""
+    torch = _torch()
+    if a.cols != b.cols:
+        raise ValueError(f"a and b must have the same number of columns: {a.cols}, {b.cols}")
+    if out is None:
+        out = torch.empty((a.rows, b.rows), dtype=out_dtype or torch.bfloat16, device=a.device)
+        yp, ldy = out.data_ptr(), max(b.rows, 1)
+    else:
+        if tuple(out.shape) != (a.rows, b.rows) or (out_dtype or out.dtype) != out.dtype:
+            raise ValueError("out must be (a.rows, b.rows) and of out_dtype")
+        yp, ldy = _matrix(out, "out") if b.rows else (0, 1)
+    _check_device(a.device, b=[b.data], out=[out])
+    _call(a.device, "muon_matmul8", a._c, b._c, yp, _dtype_code(out.dtype), ldy)
+    return out
+
+
+def weight_grad_workspace_bytes(tokens: int, n: int, k: int) -> int:
+    return int(lib().muon_weight_grad_workspace_bytes(tokens, n, k))
+
+
+def weight_grad(dy, x, *, out_dtype=None, out=None, accumulate: bool = False, workspace=None):
+    """dy^T x: the gradient (n, k) of a linear layer's weights from its output
+    gradient ``dy`` (tokens, n), bf16, and its input ``x``, a Tensor8 (tokens,
+    k).  fp32 (default) or bf16; ``accumulate`` adds to an fp32 ``out``."""
+    torch = _torch()
+    dyp, lddy = _matrix(dy, "dy")
+    tokens, n = dy.shape
+    if x.rows != tokens:
+        raise ValueError(f"dy and x must have the same number of rows: {tokens}, {x.rows}")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((n, x.cols), dtype=out_dtype or torch.float32, device=dy.device)
+    elif (tuple(out.shape) != (n, x.cols) or (out_dtype or out.dtype) != out.dtype
+          or not out.is_contiguous()):
+        raise ValueError("out must be contiguous, (dy columns, x columns), and of out_dtype")
+    _check_device(dy.device, x=[x.data], out=[out], workspace=[_raw(workspace)])
+    need = weight_grad_workspace_bytes(tokens, n, x.cols)
+    wptr, wbytes = _workspace(need, dy.device, workspace) if need else (0, 0)
+    _call(dy.device, "muon_weight_grad", dyp, _dtype_code(dy.dtype), lddy, tokens, n, x._c,
+          out.data_ptr(), _dtype_code(out.dtype), 1 if accumulate else 0, wptr, wbytes)
+    return out
+
+
+def _raw(workspace):
+    """A workspace given as a tensor, for the device check."""
+    return workspace if hasattr(workspace, "data_ptr") else None
+
+
+def layer_norm(x, weight, bias=None, *, eps: float = 1e-5, out_dtype=None):
+    """Layer norm over the last axis of ``x`` (rows, cols): (y, mean, rstd).
+    ``out_dtype`` bf16 or fp32 (default: x's), or torch.float8_e4m3fn for a
+    Tensor8 with blocks of 1 x 128.  ``weight`` and ``bias`` are fp32."""
+    torch = _torch()
+    xp, ldx = _matrix(x, "x")
+    rows, cols = x.shape
+    device = x.device
+    wp = _vector(weight, cols, "weight")
+    bp = _vector(bias, cols, "bias") if bias is not None else None
+    _check_device(device, weight=[weight], bias=[bias])
+    stats = torch.empty((2, rows), dtype=torch.float32, device=device)
+    mean, rstd = stats[0], stats[1]
+    out_dtype = out_dtype or x.dtype
+    if out_dtype == torch.float8_e4m3fn:
+        y = Tensor8.empty(rows, cols, 1, device)
+        yp, code, ldy, y8 = None, MUON_BF16, cols, y._c
+    else:
+        code = _dtype_code(out_dtype)
+        y = torch.empty((rows, cols), dtype=out_dtype, device=device)
+        yp, ldy, y8 = y.data_ptr(), cols, None
+    sp = stats.data_ptr()
+    _call(device, "muon_layer_norm", xp, _dtype_code(x.dtype), ldx, rows, cols, wp, bp, eps,
+          yp, code, ldy, y8, sp, sp + 4 * rows)
+    return y, mean, rstd
+
+
+def layer_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().muon_layer_norm_backward_workspace_bytes(rows, cols))
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, *, bias: bool = True, dweight=None,
+                        dbias=None, accumulate: bool = False, workspace=None):
+    """(dx, dweight, dbias) of layer_norm.  ``x`` is the forward pass's input,
+    or the Tensor8 that was kept of it; dx has dy's dtype.  ``dweight`` and
+    ``dbias`` (fp32) may be given, and are added to with ``accumulate``;
+    ``bias`` False: no dbias (None)."""
+    torch = _torch()
+    dyp, lddy = _matrix(dy, "dy")
+    rows, cols = dy.shape
+    device = dy.device
+    if tuple(x.shape) != (rows, cols):
+        raise ValueError("x and dy must have the same shape")
+    if isinstance(x, Tensor8):
+        xp, xcode, ldx, x8, xt = None, MUON_BF16, cols, x._c, x.data
+    else:
+        xp, ldx = _matrix(x, "x")
+        xcode, x8, xt = _dtype_code(x.dtype), None, x
+    if not bias and dbias is not None:
+        raise ValueError("dbias was given with bias=False")
+    if accumulate and (dweight is None or (bias and dbias is None)):
+        raise ValueError("accumulate needs dweight and dbias")
+    wp, mp, rp = (_vector(t, n, name) for t, n, name in (
+        (weight, cols, "weight"), (mean, rows, "mean"), (rstd, rows, "rstd")))
+    dx = torch.empty((rows, cols), dtype=dy.dtype, device=device)
+    if dweight is None:
+        dweight = torch.empty(cols, dtype=torch.float32, device=device)
+    if bias and dbias is None:
+        dbias = torch.empty(cols, dtype=torch.float32, device=device)
+    dwp = _vector(dweight, cols, "dweight")
+    dbp = _vector(dbias, cols, "dbias") if bias else None
+    _check_device(device, x=[xt], weight=[weight], mean=[mean], rstd=[rstd], dweight=[dweight],
+                  dbias=[dbias], workspace=[_raw(workspace)])
+    need = layer_norm_backward_workspace_bytes(rows, cols)
+    wptr, wbytes = _workspace(need, device, workspace) if need else (0, 0)
+    _call(device, "muon_layer_norm_backward", dyp, _dtype_code(dy.dtype), lddy, xp, xcode, ldx,
+          x8, rows, cols, wp, mp, rp, dx.data_ptr(), cols, dwp, dbp, 1 if accumulate else 0,
+          wptr, wbytes)
+    return dx, dweight, dbias

@@ -1,0 +1,542 @@
+"""The 8-bit linear layer and layer norm on the GPU against the 64-bit oracle.
+
+Bounds.  u = 2^-24 is half a step of fp32 relative to the value; an output
+in bf16 adds half a step of its own, 2^-8.  A sum of n products whose terms
+are added in any order in fp32 is off by at most n u sum|terms| to first
+order; the matrix instructions add several products at once, each of those
+additions held to one step (2 u).  matmul8's bf16 results come from an
+instruction that cuts each product off 13 bits below the largest of its
+group of 8 (measured on the chip, see CUT8).  Values taken from 8 bits are exact in fp32
+and bf16, and so are products of two of them.  Quantisation has no bound: its
+result is one number, and it has to be that one."""
+import numpy as np
+import pytest
+import torch
+
+import muon_newton_schulz_step_amd as mn
+from gpu_helpers import announce, to64
+from oracle import layers_oracle as lo
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF16, FP32, E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+U = 2.0 ** -24
+HALF = {BF16: 2.0 ** -8, FP32: U}
+EPS = 1e-5
+# A group of 8 products p_i with the largest p: each of the other 7 is cut to a
+# multiple of 2^-13 times the power of two at or below |p|, so it loses less
+# than 2^-13 |p| <= 2^-13 sum |p_i|.  Over all groups: less than 7 * 2^-13 times
+# the sum of all products' magnitudes.  (fp32 alone, 2 (k + 1) u of that sum, was
+# exceeded by up to 1.23 times at k = 129 when fp32 results came from this
+# instruction; they no longer do.)
+CUT8 = 7 * 2.0 ** -13
+
+
+def randn(*shape, seed=0, std=1.0, dtype=FP32):
+    g = torch.Generator(DEV).manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device=DEV) * std).to(dtype)
+
+
+def parts(t):
+    """(e4m3 numbers, exponents, values) of a Tensor8, 64 bits, on the host."""
+    nb = -(-t.cols // 128)
+    q = to64(t.data.float())[:, :t.cols]
+    e = t.scale.cpu().numpy().astype(np.int64)[:, :nb] - 127
+    return q, e, q * lo.expand(e, q.shape, t.block_rows)
+
+
+def check8(t, x, block_rows):
+    q, e = lo.quantize8(to64(x), block_rows)
+    got_q, got_e, _ = parts(t)
+    assert np.array_equal(got_e, e)
+    assert np.array_equal(got_q, q, equal_nan=True)
+    pad = t.data.view(torch.uint8)[:, t.cols:]
+    assert torch.count_nonzero(pad) == 0
+
+
+def within(got, ref, bound):
+    got = to64(got.float()) if torch.is_tensor(got) else got
+    assert got.shape == ref.shape
+    bad = ~(np.abs(got - ref) <= bound)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(),
+                           float(np.nanmax(np.abs(got - ref) / np.maximum(bound, 1e-300))))
+
+
+# ------------------------------------------------------------ 8-bit tensors
+SHAPES8 = [(1, 1), (1, 127), (3, 128), (2, 129), (5, 515), (130, 640), (257, 1283)]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("rows,cols", SHAPES8)
+def test_quantize8(rows, cols, block_rows, dtype):
+    announce("quantize8", rows, cols, block_rows, dtype)
+    x = randn(rows, cols, seed=rows + cols, dtype=FP32) * torch.exp2(randn(rows, cols, seed=1) * 4)
+    x = x.to(dtype)
+    t = mn.quantize8(x, block_rows)
+    check8(t, x, block_rows)
+    for out in (BF16, FP32):
+        assert np.array_equal(to64(mn.dequantize8(t, out)), parts(t)[2])
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("rows,cols", SHAPES8)
+def test_quantize8_transposed(rows, cols, dtype):
+    announce("quantize8 transposed", rows, cols, dtype)
+    x = randn(rows, cols, seed=7, dtype=dtype)
+    t, tt = mn.quantize8(x, 128, transposed=True)
+    check8(t, x, 128)
+    check8(tt, x.t(), 128)
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_quantize8_special_values(dtype, block_rows):
+    announce("quantize8 special values", dtype, block_rows)
+    x = randn(129, 520, seed=3, dtype=FP32)
+    x[0] = 0.0                                       # a block of zeros
+    x[1, :128] = torch.linspace(-448, 448, 128, device=DEV)
+    x[2, 5], x[2, 300], x[2, 301] = float("inf"), float("nan"), float("-inf")
+    x[3] = float("nan")                              # nothing finite in the row
+    x[4] *= 1e-36
+    x[5] *= 1e-42                                    # subnormal
+    x[6, 17] = 3e38
+    x[7, :16] = torch.tensor([448.0, 449, 464, 17, 19, 0.5, 0.53125, 2.0 ** -9, 2.0 ** -10,
+                              3 * 2.0 ** -10, 2.0 ** -11, -17, -19, 1.0625, 1.1875, -0.0], device=DEV)
+    x[8], x[8, 0] = 1e-6, 3e38                       # far below the block's largest
+    x = x.to(dtype)
+    check8(mn.quantize8(x, block_rows), x, block_rows)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_quantize8_row_stride(dtype):
+    announce("quantize8 of strided rows", dtype)
+    whole = randn(131, 389, seed=4, dtype=dtype)
+    x = whole[:, 8:8 + 200]                          # rows begin at any element
+    check8(mn.quantize8(x), x, 1)
+    t, tt = mn.quantize8(x, 128, transposed=True)
+    check8(t, x, 128)
+    check8(tt, x.t(), 128)
+    assert mn.quantize8(x[:0]).shape == (0, 200)
+    check8(mn.quantize8(whole[5:6]), whole[5:6], 1) if whole[5:6].data_ptr() % 16 == 0 else None
+
+
+# ------------------------------------------------------------ products
+def product_case(m, n, k, ba, bb, out, seed=0):
+    announce("matmul8", m, n, k, ba, bb, out)
+    a = mn.quantize8(randn(m, k, seed=seed) * torch.exp2(3 * randn(m, 1, seed=seed + 1)), ba)
+    b = mn.quantize8(randn(n, k, seed=seed + 2, std=0.02), bb)
+    y = mn.matmul8(a, b, out_dtype=out)
+    assert y.shape == (m, n) and y.dtype == out
+    av, bv = parts(a)[2], parts(b)[2]
+    ref, mag = av @ bv.T, np.abs(av) @ np.abs(bv).T
+    bound = 2 * U * (k + 1) * mag
+    if out == BF16:
+        bound = bound + (CUT8 * mag if m > 64 else 0.0)
+        bound = bound + HALF[BF16] * (np.abs(ref) + bound)
+        # the roundings to bf16 are independent and uniform: 2^-9 relative at most
+        # in the root mean square (2^-8 / sqrt(3) of a value just above a power
+        # of two); with 7 cut products a group at their bound's root mean square
+        if ref.size > 1000:
+            assert np.linalg.norm(to64(y.float()) - ref) <= 2.0 ** -8 / 3 ** 0.5 * np.linalg.norm(ref)
+    within(y, ref, bound + 1e-300)
+    assert torch.equal(y, mn.matmul8(a, b, out_dtype=out))  # the same every time
+    return a, b, y
+
+
+@pytest.mark.parametrize("out", [BF16, FP32])
+@pytest.mark.parametrize("m,n,k", [
+    (1, 1, 1), (1, 15, 128), (1, 1283, 770), (2, 100, 515), (16, 16, 256), (17, 33, 1283), (32, 257, 130),
+    (33, 64, 640), (64, 300, 2050), (65, 1, 128), (65, 129, 300), (100, 259, 129), (128, 128, 128),
+    (129, 511, 896), (300, 1000, 1283), (1000, 77, 513)])
+def test_matmul8(m, n, k, out):
+    product_case(m, n, k, 1, 128, out, seed=m)
+
+
+@pytest.mark.parametrize("ba,bb", [(1, 1), (128, 1), (128, 128)])
+@pytest.mark.parametrize("m", [5, 40, 131])
+def test_matmul8_blocks(m, ba, bb):
+    product_case(m, 385, 700, ba, bb, FP32, seed=m)
+
+
+@pytest.mark.parametrize("m,n,k", [(4099, 4097, 385), (3841, 4352, 128), (16385, 1100, 200)])
+def test_matmul8_large_grids(m, n, k):
+    product_case(m, n, k, 1, 128, BF16)
+
+
+def test_matmul8_row_stride_and_non_finite():
+    announce("matmul8 strided output, NaN rows")
+    for m in (3, 70, 200):
+        x, w = randn(m, 300, seed=1), randn(130, 300, seed=2)
+        x[1, 7], w[100, 299] = float("inf"), float("nan")
+        a, b = mn.quantize8(x), mn.quantize8(w)
+        whole = torch.full((m + 1, 200), 7.0, device=DEV, dtype=BF16)
+        mn.matmul8(a, b, out=whole[:m, 16:146])
+        y = mn.matmul8(a, b)
+        bad = torch.zeros(m, 130, dtype=torch.bool, device=DEV)
+        bad[1], bad[:, 100] = True, True
+        assert torch.equal(y.isnan(), bad)
+        assert torch.equal(whole[:m, 16:146].nan_to_num(9.0), y.nan_to_num(9.0))
+        assert (whole[:, :16] == 7).all() and (whole[:, 146:] == 7).all() and (whole[m] == 7).all()
+    assert mn.matmul8(mn.quantize8(x[:0]), b).shape == (0, 130)
+    assert mn.matmul8(a, mn.quantize8(w[:0])).shape == (m, 0)
+
+
+# ------------------------------------------------------------ weight gradient
+def weight_grad_case(tokens, n, k, out=FP32, block_rows=1, seed=0, **kw):
+    announce("weight_grad", tokens, n, k, out, block_rows)
+    dy = randn(tokens, n, seed=seed, std=1e-3, dtype=BF16)
+    x = mn.quantize8(randn(tokens, k, seed=seed + 1) * torch.exp2(2 * randn(tokens, 1, seed=seed + 2)),
+                     block_rows)
+    dw = mn.weight_grad(dy, x, out_dtype=out, **kw)
+    d, v = to64(dy), parts(x)[2]
+    ref, bound = d.T @ v, 2 * U * (tokens + 2) * (np.abs(d).T @ np.abs(v))
+    if out == BF16:
+        bound = bound + HALF[BF16] * (np.abs(ref) + bound)
+    within(dw, ref, bound + 1e-300)
+    return dy, x, dw
+
+
+@pytest.mark.parametrize("out", [BF16, FP32])
+@pytest.mark.parametrize("tokens,n,k", [
+    (0, 5, 7), (1, 1, 1), (1, 300, 130), (63, 128, 128), (64, 129, 257), (65, 130, 1283), (500, 77, 515),
+    (1000, 256, 256), (4097, 100, 33), (9000, 130, 260), (2000, 1283, 770)])
+def test_weight_grad(tokens, n, k, out):
+    dy, x, dw = weight_grad_case(tokens, n, k, out, seed=tokens)
+    assert torch.equal(dw, mn.weight_grad(dy, x, out_dtype=out))
+
+
+@pytest.mark.parametrize("tokens", [0, 1, 100, 9000])
+def test_weight_grad_accumulates(tokens):
+    n, k = 130, 200
+    dy, x, dw = weight_grad_case(tokens, n, k)
+    for start in (0.0, 3.0):
+        acc = torch.full((n, k), start, device=DEV)
+        assert mn.weight_grad(dy, x, out=acc, accumulate=True) is acc
+        assert torch.equal(acc, start + dw)
+        mn.weight_grad(dy, x, out=acc, accumulate=True)
+        assert torch.equal(acc, (start + dw) + dw)
+
+
+def test_weight_grad_strided_and_128_row_blocks():
+    weight_grad_case(333, 140, 260, block_rows=128)
+    announce("weight_grad strided dy")
+    whole = randn(333, 331, seed=5, dtype=BF16)
+    x = mn.quantize8(randn(333, 140, seed=6))
+    assert torch.equal(mn.weight_grad(whole[:, 8:108], x), mn.weight_grad(whole[:, 8:108].contiguous(), x))
+
+
+def test_weight_grad_keeps_non_finite_rows_apart():
+    announce("weight_grad NaN")
+    dy, x = randn(130, 40, seed=1, dtype=BF16), randn(130, 50, seed=2)
+    x[129, 3], dy[0, 7] = float("nan"), float("inf")
+    dw = mn.weight_grad(dy, mn.quantize8(x))
+    bad = torch.zeros(40, 50, dtype=torch.bool, device=DEV)
+    bad[:, 3], bad[7] = True, True
+    assert torch.equal(~dw.isfinite(), bad)
+
+
+# ------------------------------------------------------------ layer norm
+COLS = [1, 2, 7, 127, 512, 513, 1025, 1283, 1537, 2048, 2049, 4099, 6145, 8193, 16384]
+
+
+def norm_inputs(rows, cols, dtype, seed=0):
+    x = (randn(rows, cols, seed=seed) * torch.exp2(2 * randn(rows, 1, seed=seed + 1)) + 0.3).to(dtype)
+    return x, 1 + 0.3 * randn(cols, seed=seed + 2), 0.2 * randn(cols, seed=seed + 3)
+
+
+def forward_bounds(x, w, b, mean, rstd, cols):
+    """First-order error of each stage: sums in a tree whose longest path has
+    at most d additions (32 values of a lane, 6 exchanges, 16 waves)."""
+    d = min(cols, 32) + 6 + 16
+    mu = (d + 1) * U * np.abs(x).mean(1)                     # the mean
+    xc = x - mean[:, None]
+    dxc = mu[:, None] + U * np.abs(xc)                       # x - mean
+    var = (xc ** 2).mean(1)
+    dvar = 2 * (np.abs(xc) * dxc).mean(1) + (d + 3) * U * var + mu ** 2
+    rel = 0.5 * dvar / (var + EPS) + 4 * U                   # rstd: sqrt and division
+    xh = np.abs(xc) * rstd[:, None]
+    y = np.abs(w) * (xh * (rel[:, None] + 4 * U) + dxc * rstd[:, None])
+    return mu, rel * rstd, y + U * np.abs(xc * rstd[:, None] * w + b)
+
+
+@pytest.mark.parametrize("cols", COLS)
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (FP32, FP32), (FP32, BF16), (BF16, FP32)])
+def test_layer_norm(cols, dtype, out):
+    for rows in (1, 5):
+        announce("layer_norm", rows, cols, dtype, out)
+        x, w, b = norm_inputs(rows, cols, dtype, seed=cols)
+        for bias in (b, None):
+            y, mean, rstd = mn.layer_norm(x, w, bias, eps=EPS, out_dtype=out)
+            x64, w64 = to64(x), to64(w)
+            b64 = to64(bias) if bias is not None else np.zeros(cols)
+            ry, rm, rr = lo.layer_norm(x64, w64, b64, EPS)
+            bm, br, by = forward_bounds(x64, w64, b64, rm, rr, cols)
+            within(mean, rm, bm + 1e-45)
+            within(rstd, rr, br)
+            within(y, ry, by + HALF[out] * (np.abs(ry) + by) + 1e-45)
+
+
+def test_layer_norm_many_rows_and_strides():
+    for rows, cols in ((9001, 300), (2500, 2500), (700, 9000)):
+        announce("layer_norm", rows, cols, "strided")
+        whole = randn(rows, cols + 13, seed=1, dtype=BF16)
+        w, b = 1 + 0.3 * randn(cols, seed=2), 0.2 * randn(cols, seed=3)
+        x = whole[:, 8:8 + cols]
+        y, mean, rstd = mn.layer_norm(x, w, b, eps=EPS, out_dtype=FP32)
+        ry, rm, rr = lo.layer_norm(to64(x), to64(w), to64(b), EPS)
+        bm, br, by = forward_bounds(to64(x), to64(w), to64(b), rm, rr, cols)
+        within(mean, rm, bm)
+        within(rstd, rr, br)
+        within(y, ry, by + U * np.abs(ry))
+        dy = randn(rows, cols + 5, seed=4, dtype=BF16)[:, :cols]
+        got = mn.layer_norm_backward(dy, x, w, mean, rstd)
+        check_backward(got, dy, to64(x), w, mean, rstd)
+
+
+@pytest.mark.parametrize("cols", COLS)
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_layer_norm_to_8_bits(cols, dtype):
+    # the same rows in fp32, rounded on the host: one number, as for quantize8
+    announce("layer_norm to 8 bits", cols, dtype)
+    x, w, b = norm_inputs(7, cols, dtype, seed=cols)
+    t, mean, rstd = mn.layer_norm(x, w, b, eps=EPS, out_dtype=E4M3)
+    y, mean2, rstd2 = mn.layer_norm(x, w, b, eps=EPS, out_dtype=FP32)
+    check8(t, y, 1)
+    assert torch.equal(mean, mean2) and torch.equal(rstd, rstd2)
+
+
+def test_layer_norm_non_finite_rows_and_equal_rows():
+    announce("layer_norm non-finite rows")
+    x, w, b = norm_inputs(9, 300, FP32)
+    clean = mn.layer_norm(x, w, b, eps=EPS)[0].clone()
+    x[2, 5], x[4, 299] = float("nan"), float("inf")
+    x[7] = 2.5                                      # no variance: y = bias
+    for out in (FP32, E4M3):
+        y = mn.layer_norm(x, w, b, eps=EPS, out_dtype=out)[0]
+        y = y if out == FP32 else mn.dequantize8(y, FP32)
+        bad = y.isnan().all(1)
+        assert bad.nonzero().flatten().tolist() == [2, 4] and torch.equal(bad, y.isnan().any(1))
+        if out == FP32:
+            keep = [0, 1, 3, 5, 6, 8]
+            assert torch.equal(y[keep], clean[keep]) and torch.equal(y[7], b)
+
+
+def check_backward(got, dy, x64, w, mean, rstd, start=0.0):
+    dx, dw, db = got
+    d, w64, m64, r64 = to64(dy), to64(w), to64(mean), to64(rstd)
+    rows, cols = d.shape
+    rx, rw, rb = lo.layer_norm_backward(d, x64, w64, m64, r64)
+    t = min(cols, 32) + 6 + 16
+    r = r64[:, None]
+    xh = np.abs(x64 - m64[:, None]) * r
+    g = np.abs(d * w64)
+    c0, c1 = g.mean(1, keepdims=True), (g * xh).mean(1, keepdims=True)
+    # xh is off by 2 u of itself, g by u; the sums by t additions
+    bx = r * (4 * U * g + (t + 4) * U * c0 + xh * c1 * (t + 8) * U)
+    within(dx, rx, bx + HALF[dy.dtype] * (np.abs(rx) + bx) + 1e-45)
+    n = rows + 1
+    within(dw, rw + start, 1e-45 + (n + 4) * U * (np.abs(d) * xh).sum(0) + U * abs(start) * 2)
+    within(db, rb + start, 1e-45 + n * U * np.abs(d).sum(0) + U * abs(start) * 2)
+
+
+@pytest.mark.parametrize("cols", COLS)
+@pytest.mark.parametrize("kept", ["bf16", "fp32", "fp8", "fp8 blocks"])
+def test_layer_norm_backward(cols, kept):
+    for rows, dtype in ((1, FP32), (6, BF16), (150, FP32)):
+        announce("layer_norm_backward", rows, cols, kept, dtype)
+        x, w, b = norm_inputs(rows, cols, BF16 if kept == "bf16" else FP32, seed=cols)
+        _, mean, rstd = mn.layer_norm(x, w, b, eps=EPS)
+        dy = randn(rows, cols, seed=9, dtype=dtype)
+        if kept.startswith("fp8"):
+            x = mn.quantize8(x, 128 if "blocks" in kept else 1)
+            x64 = parts(x)[2]
+        else:
+            x64 = to64(x)
+        got = mn.layer_norm_backward(dy, x, w, mean, rstd)
+        check_backward(got, dy, x64, w, mean, rstd)
+        again = mn.layer_norm_backward(dy, x, w, mean, rstd)
+        assert all(torch.equal(p, q) for p, q in zip(got, again))
+
+
+def test_layer_norm_backward_accumulates():
+    announce("layer_norm_backward accumulate")
+    for rows in (0, 1, 500):
+        x, w, b = norm_inputs(rows, 700, FP32)
+        _, mean, rstd = mn.layer_norm(x, w, b, eps=EPS)
+        dy = randn(rows, 700, seed=9)
+        _, dw, db = mn.layer_norm_backward(dy, x, w, mean, rstd)
+        if rows == 0:
+            assert torch.count_nonzero(dw) == 0 and torch.count_nonzero(db) == 0
+        aw, ab = torch.full_like(dw, 2.0), torch.full_like(db, 2.0)
+        mn.layer_norm_backward(dy, x, w, mean, rstd, dweight=aw, dbias=ab, accumulate=True)
+        assert torch.equal(aw, 2.0 + dw) and torch.equal(ab, 2.0 + db)
+        dx, only, none = mn.layer_norm_backward(dy, x, w, mean, rstd, bias=False)
+        assert none is None and torch.equal(only, dw)
+
+
+# ------------------------------------------------------------ together
+def layer(x, g, b, W, dy, buf, dW):
+    """One linear layer behind a layer norm: forward, backward, two micro-batches'
+    gradient, the step of the weights, their 8-bit copies for the next."""
+    w8, w8t = mn.quantize8(W, 128, transposed=True)
+    h8, mean, rstd = mn.layer_norm(x, g, b, eps=EPS, out_dtype=E4M3)
+    y = mn.matmul8(h8, w8)
+    dh = mn.matmul8(mn.quantize8(dy), w8t)
+    dx, dg, db = mn.layer_norm_backward(dh, x, g, mean, rstd)
+    mn.weight_grad(dy, h8, out=dW)
+    mn.weight_grad(dy, h8, out=dW, accumulate=True)
+    mn.step([W], [dW], [buf], mu=0.95, lr=0.02)
+    return h8, mean, rstd, y, dh, dx, dg, db, mn.quantize8(W, 128, transposed=True)
+
+
+def layer_inputs(tokens=333, n=260, k=515):
+    x, g, b = norm_inputs(tokens, k, BF16, seed=11)
+    return [x, g, b, randn(n, k, seed=21, std=0.02), randn(tokens, n, seed=22, std=1e-2, dtype=BF16),
+            torch.zeros(n, k, device=DEV), torch.zeros(n, k, device=DEV)]
+
+
+def test_layer_end_to_end():
+    announce("a layer, forward to step")
+    args = layer_inputs()
+    x, g, b, W, dy, buf, dW = args
+    W0 = W.clone()
+    w8, w8t = mn.quantize8(W0, 128, transposed=True)
+    h8, mean, rstd, y, dh, dx, dg, db, (n8, n8t) = layer(*args)
+    hv, wv = parts(h8)[2], parts(w8)[2]
+    mag = np.abs(hv) @ np.abs(wv).T
+    within(y, hv @ wv.T, (2 * U * 516 + CUT8) * mag * 1.01 + HALF[BF16] * np.abs(hv @ wv.T))
+    dv, tv = parts(mn.quantize8(dy))[2], parts(w8t)[2]
+    assert np.array_equal(tv, wv.T)
+    mag = np.abs(dv) @ np.abs(wv)
+    within(dh, dv @ wv, (2 * U * 261 + CUT8) * mag * 1.01 + HALF[BF16] * np.abs(dv @ wv))
+    check_backward((dx, dg, db), dh, to64(x), g, mean, rstd)
+    d = to64(dy)
+    within(dW, 2 * (d.T @ hv), 2 * U * 340 * 2 * (np.abs(d).T @ np.abs(hv)))
+    # the step takes the gradient, and the new weights are what is quantised
+    want = W0.clone()
+    mn.step([want], [dW], [torch.zeros_like(buf)], mu=0.95, lr=0.02)
+    assert torch.equal(W, want) and not torch.equal(W, W0)
+    check8(n8, W, 128)
+    check8(n8t, W.t(), 128)
+
+
+def test_gradients_against_differences():
+    # of the 64-bit loss sum(dy * layer_norm(x) W^T) in x, g, b and W; the
+    # 8-bit steps make each value differ from the exact gradient's by up to
+    # 2^-4 of an operand's magnitude, so a projection on a random direction,
+    # of N terms with independent errors, is off by about 2^-4 of their
+    # 2-norm and stays within 8 times that
+    announce("gradients against differences")
+    args = layer_inputs(200, 130, 260)
+    x, g, b, W, dy, buf, dW = args
+    vals = [to64(t) for t in (x, g, b, W)]
+    d = to64(dy)
+
+    def loss(x, g, b, w):
+        return (d * (lo.layer_norm(x, g, b, EPS)[0] @ w.T)).sum()
+
+    W0 = W.clone()
+    _, mean, rstd, _, dh, dx, dg, db, _ = layer(*args)
+    mn.weight_grad(dy, mn.layer_norm(x, g, b, eps=EPS, out_dtype=E4M3)[0], out=dW)
+    vals[3] = to64(W0)
+    rng = np.random.default_rng(0)
+    for which, got in enumerate((dx, dg, db, dW)):
+        v = rng.normal(size=vals[which].shape)
+        hi, lw = list(vals), list(vals)
+        hi[which], lw[which] = vals[which] + 1e-4 * v, vals[which] - 1e-4 * v
+        diff = (loss(*hi) - loss(*lw)) / 2e-4
+        terms = to64(got) * v
+        assert abs(diff - terms.sum()) <= 8 * 2.0 ** -4 * np.linalg.norm(terms), which
+
+
+def outputs_of(result):
+    out = []
+    for r in result:
+        for t in (r if isinstance(r, tuple) else (r,)):
+            out += [t.data.view(torch.uint8), t.scale] if isinstance(t, mn.Tensor8) else [t]
+    return out
+
+
+def test_layer_captured_replays_match_eager():
+    announce("a layer, captured")
+    args, eager = layer_inputs(2000), layer_inputs(2000)
+    layer(*layer_inputs(2000))  # the stream's workspace has its size
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = layer(*args)
+    torch.cuda.synchronize()
+    for replay in range(4):
+        graph.replay()
+        want = layer(*eager)
+        torch.cuda.synchronize()
+        for p, q in zip(outputs_of(captured) + [args[3], args[6]], outputs_of(want) + [eager[3], eager[6]]):
+            assert torch.equal(p, q), replay
+        torch.randn(1 << 20, device=DEV).square().sum().item()
+    del graph
+
+
+def test_two_streams_at_once():
+    announce("two streams at once")
+    want = [outputs_of(layer(*layer_inputs(t))) for t in (1500, 700)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    args = [layer_inputs(t) for t in (1500, 700)]
+    torch.cuda.synchronize()
+    got = []
+    for s, a in zip(streams, args):
+        with torch.cuda.stream(s):
+            got.append(layer(*a))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for p, q in zip(outputs_of(g), w):
+            assert torch.equal(p, q)
+
+
+def test_timing_log_names_the_launches():
+    announce("timing log")
+    mn.timing_read()
+    mn.timing_enable(True)
+    layer(*layer_inputs(100))
+    mn.timing_enable(False)
+    kinds = [r["kind"] for r in mn.timing_read()]
+    assert kinds.count("quant8") == 3 and kinds.count("matmul8") == 2
+    assert kinds.count("weight_grad") == 2
+    assert kinds.count("layer_norm") == kinds.count("layer_norm_back") == 1
+
+
+def test_offsets_past_32_bits():
+    # 2^31 values and more: the last rows against the same rows on their own
+    announce("offsets past 32 bits: quantize8")
+    rows, cols = 40000, 65536
+    g = torch.Generator(DEV).manual_seed(1)
+    x = torch.empty(rows, cols, dtype=BF16, device=DEV).normal_(generator=g)
+    t = mn.quantize8(x)
+    tail = mn.quantize8(x[-3:].contiguous())
+    assert torch.equal(t.data[-3:].view(torch.uint8), tail.data.view(torch.uint8))
+    assert torch.equal(t.scale[-3:], tail.scale)
+    announce("offsets past 32 bits: dequantize8")
+    assert torch.equal(mn.dequantize8(t)[-3:], mn.dequantize8(tail))
+    announce("offsets past 32 bits: matmul8")
+    b = mn.quantize8(randn(70, cols, seed=2, std=0.02))
+    y = mn.matmul8(t, b, out_dtype=FP32)
+    av, bv = parts(tail)[2], parts(b)[2]
+    within(y[-3:], av @ bv.T, 2 * U * (cols + 1) * (np.abs(av) @ np.abs(bv).T))
+    y = mn.matmul8(b, t, out_dtype=FP32)
+    within(y[:, -3:].contiguous(), bv @ av.T, 2 * U * (cols + 1) * (np.abs(bv) @ np.abs(av).T))
+    announce("offsets past 32 bits: weight_grad")
+    dy = torch.zeros(rows, 8, dtype=BF16, device=DEV)
+    dy[-3:] = randn(3, 8, seed=3).bfloat16()
+    dw = mn.weight_grad(dy, t)
+    d = to64(dy[-3:])
+    within(dw, d.T @ av, 2 * U * (rows + 2) * (np.abs(d).T @ np.abs(av)))
+    del t, y, dw
+    announce("offsets past 32 bits: layer_norm")
+    x = x.view(-1, 16384)
+    w = torch.ones(16384, device=DEV)
+    y, mean, rstd = mn.layer_norm(x, w)
+    small = mn.layer_norm(x[-3:].contiguous(), w)
+    assert torch.equal(y[-3:], small[0]) and torch.equal(rstd[-3:], small[2])
+    dx, _, _ = mn.layer_norm_backward(x, y, w, mean, rstd)
+    sx, _, _ = mn.layer_norm_backward(x[-3:].contiguous(), y[-3:].contiguous(), w, mean[-3:].contiguous(),
+                                      rstd[-3:].contiguous())
+    assert torch.equal(dx[-3:], sx)

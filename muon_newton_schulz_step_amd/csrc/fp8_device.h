@@ -102,16 +102,25 @@ __device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
   const bf16x2_t p = {static_cast<bf16_t>(lo), static_cast<bf16_t>(hi)};
   return __builtin_bit_cast(unsigned, p);
 }
+template <bool STRM>
+__device__ __forceinline__ void store16(void* p, u32x4_t v) {
+  typedef u32x4_t __attribute__((aligned(2))) any_t;
+  if constexpr (STRM)
+    __builtin_nontemporal_store(v, static_cast<any_t*>(p));
+  else
+    *static_cast<any_t*>(p) = v;
+}
+template <bool STRM = false>
 __device__ __forceinline__ void store8(bf16_t* p, const float (&v)[8]) {
   u32x4_t w;
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-  __builtin_memcpy(p, &w, 16);
+  store16<STRM>(p, w);
 }
+template <bool STRM = false>
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  const f32x4_t a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
-  __builtin_memcpy(p, &a, 16);
-  __builtin_memcpy(p + 4, &b, 16);
+  store16<STRM>(p, __builtin_bit_cast(u32x4_t, f32x4_t{v[0], v[1], v[2], v[3]}));
+  store16<STRM>(p + 4, __builtin_bit_cast(u32x4_t, f32x4_t{v[4], v[5], v[6], v[7]}));
 }
 // The first `n` of eight elements (n <= 0: none); the others read as zero.
 template <typename T>
@@ -123,15 +132,25 @@ __device__ __forceinline__ void load8_edge(const T* p, int n, float (&v)[8]) {
     for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
   }
 }
-template <typename T>
+// STRM: streamed past the caches.
+template <bool STRM = false, typename T>
 __device__ __forceinline__ void store8_edge(T* p, int n, const float (&v)[8]) {
   if (n >= 8) {
-    store8(p, v);
+    store8<STRM>(p, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (i < n) p[i] = from_f32<T>(v[i]);
   }
+}
+
+// 4 bytes per lane from global memory straight into LDS (see buffer_load_lds16).
+__device__ __forceinline__ void buffer_load_lds4(__amdgpu_buffer_rsrc_t rsrc, unsigned voffset,
+                                                 void* lds_wave_base) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(
+      rsrc, (__attribute__((address_space(3))) void*)lds_wave_base, 4, (int)voffset, 0, 0, 0);
+#endif
 }
 
 // Maximum over each row of 16 lanes, in all of them (DPP rotations).

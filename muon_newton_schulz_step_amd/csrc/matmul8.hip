@@ -40,20 +40,35 @@ __device__ __forceinline__ i32x8_t frag8(const u32x4_t& lo, const u32x4_t& hi) {
 // loaded straight into LDS, two stages.  A substep is 64 k, one 32x32x64
 // MFMA or (EXACT) four 32x32x16: lane (r, h) = (lane % 32, lane / 32) reads
 // chunks 4 kk + 2 h and the one after it of its row, for both operands the
-// same, so the order of k does not matter.  Rows past the last one read the last one
-// again and are not stored.
-template <int BM, int BN, int WGM, int WGN, bool EXACT, typename Y>
+// same, so the order of k does not matter.  Rows past the last one read the
+// last one again and are not stored.
+//
+// The scales go through LDS as well, a word of four k-tiles per row, so that
+// no load into registers is in flight in the main loop: the compiler's wait
+// for such a load would wait for the LDS loads too (8192 x 4096 x 4096: 114 ->
+// 108 us).  Four k-tiles are written out, because the byte of the word that an
+// MFMA takes is part of the instruction.
+//
+// The order of MFMAs, LDS reads and loads is pinned: each MFMA of a substep is
+// followed by two reads of the next one's operands, and after the barrier by
+// one load.  Between the barrier and the next wait the wave has priority over
+// its neighbour, so that the two waves of a SIMD fall out of step and one's
+// MFMAs cover the other's waits (16384 x 16384 x 4096: 874 -> 822 us).
+template <int BM, int BN, int WGM, int WGN, bool EXACT, bool STRM, typename Y>
 __global__ __launch_bounds__(64 * WGM * WGN) void matmul8_tile_kernel(Matmul8Args g) {
   constexpr int NW = WGM * WGN;
   constexpr int WTM = BM / WGM, WTN = BN / WGN;
   constexpr int FM = WTM / 32, FN = WTN / 32;
   constexpr int CPR = 8;
   constexpr int B_CHUNKS = BN * CPR, STAGE = (BM + BN) * CPR;
-  constexpr int DPW = STAGE / 64 / NW;
+  constexpr int DPW = STAGE / 64 / NW;      // loads of a wave per k-tile
+  constexpr int SPW = (BM + BN) / 64 / NW;  // and of scale words per four
   static_assert(DPW * 64 * NW == STAGE && B_CHUNKS % (DPW * 64) == 0, "one operand per wave");
+  static_assert(SPW * 64 * NW == BM + BN && BN % (SPW * 64) == 0, "one operand's scales per wave");
   // the epilogue's staging: 32 rows m of half the wave's columns, per wave
   static_assert(FN % 2 == 0 && NW * 32 * (WTN / 2) * 4 <= STAGE * 16, "staging fits");
   __shared__ u32x4_t S0[STAGE], S1[STAGE];
+  __shared__ unsigned C0[BM + BN], C1[BM + BN];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave / WGN, wn = wave % WGN;
@@ -75,28 +90,29 @@ __global__ __launch_bounds__(64 * WGM * WGN) void matmul8_tile_kernel(Matmul8Arg
     const int r = q / CPR, rl = is_b ? r : r - BN;
     voff[d] = (unsigned)(rl < last_row ? rl : last_row) * (unsigned)g.ld + swz(q % CPR, r) * 16;
   }
-  auto issue = [&](int kt, u32x4_t* St) {
+  const int nk = g.ld / 128, last_word = (nk - 1) / 4;
+  auto issue = [&](int kt, u32x4_t* St) __attribute__((always_inline)) {
     const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(base + (long long)kt * 128);
 #pragma unroll
     for (int d = 0; d < DPW; ++d) buffer_load_lds16(rs, voff[d], St + (wave_s * DPW + d) * 64);
   };
-
-  // scales of the lane's rows: a word holds those of four k-tiles
-  const unsigned* ps[FN + FM];
-  unsigned sc[FN + FM], sc_next[FN + FM];
+  // word w of the scales of the tile's rows: b's, then a's
+  const bool sc_b = wave_s * SPW * 64 < BN;
+  const int s_first = sc_b ? n0 : m0, s_last = sc_b ? g.n - 1 : g.m - 1;
+  const int s_shift = sc_b ? g.shift_b : g.shift_a;
+  const unsigned char* sbase = (sc_b ? g.sb : g.sa) + (long long)(s_first >> s_shift) * g.sld;
+  unsigned soff[SPW];
 #pragma unroll
-  for (int f = 0; f < FN; ++f) {
-    const int r = n0 + wn * WTN + f * 32 + (lane & 31);
-    ps[f] = reinterpret_cast<const unsigned*>(
-        g.sb + (long long)((r < g.n ? r : g.n - 1) >> g.shift_b) * g.sld);
+  for (int d = 0; d < SPW; ++d) {
+    const int i = (wave * SPW + d) * 64 + lane, r = s_first + (sc_b ? i : i - BN);
+    soff[d] = (unsigned)(((r < s_last ? r : s_last) >> s_shift) - (s_first >> s_shift)) *
+              (unsigned)g.sld;
   }
+  auto issue_scales = [&](int w, unsigned* C) __attribute__((always_inline)) {
+    const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(sbase + 4 * (w < last_word ? w : last_word));
 #pragma unroll
-  for (int f = 0; f < FM; ++f) {
-    const int r = m0 + wm * WTM + f * 32 + (lane & 31);
-    ps[FN + f] = reinterpret_cast<const unsigned*>(
-        g.sa + (long long)((r < g.m ? r : g.m - 1) >> g.shift_a) * g.sld);
-  }
-  const int nk = g.ld / 128, last_word = (nk - 1) / 4;
+    for (int d = 0; d < SPW; ++d) buffer_load_lds4(rs, soff[d], C + (wave_s * SPW + d) * 64);
+  };
 
   f32x16_t acc[FN][FM];
 #pragma unroll
@@ -109,24 +125,30 @@ __global__ __launch_bounds__(64 * WGM * WGN) void matmul8_tile_kernel(Matmul8Arg
   const int brow = wn * WTN + (lane & 31), arow = BN + wm * WTM + (lane & 31);
   const int hsel = lane >> 5;
   i32x8_t fb[2][FN], fa[2][FM];
-  auto fload = [&](const u32x4_t* St, int kk, int slot) {
+  int sc[FN + FM];
+  auto fload = [&](const u32x4_t* St, int kk, int slot) __attribute__((always_inline)) {
     const int ch = 4 * kk + 2 * hsel;
+    auto row = [&](int r) __attribute__((always_inline)) {
+      return frag8(St[r * CPR + swz(ch, r)], St[r * CPR + swz(ch + 1, r)]);
+    };
+    fb[slot][0] = row(brow);
 #pragma unroll
-    for (int f = 0; f < FN; ++f) {
-      const int r = brow + f * 32;
-      fb[slot][f] = frag8(St[r * CPR + swz(ch, r)], St[r * CPR + swz(ch + 1, r)]);
-    }
+    for (int f = 0; f < FM; ++f) fa[slot][f] = row(arow + f * 32);
 #pragma unroll
-    for (int f = 0; f < FM; ++f) {
-      const int r = arow + f * 32;
-      fa[slot][f] = frag8(St[r * CPR + swz(ch, r)], St[r * CPR + swz(ch + 1, r)]);
-    }
+    for (int f = 1; f < FN; ++f) fb[slot][f] = row(brow + f * 32);
   };
-  auto mfmas = [&](int slot) {
+  auto sload = [&](const unsigned* C) __attribute__((always_inline)) {
+#pragma unroll
+    for (int f = 0; f < FN; ++f) sc[f] = (int)C[brow + f * 32];
+#pragma unroll
+    for (int f = 0; f < FM; ++f) sc[FN + f] = (int)C[arow + f * 32];
+  };
+  auto mfmas = [&](int slot, auto byte) __attribute__((always_inline)) {
+    constexpr int B = decltype(byte)::value;
     if constexpr (EXACT) {
       float sf[FN + FM];
 #pragma unroll
-      for (int f = 0; f < FN + FM; ++f) sf[f] = scale_of((int)(sc[f] & 0xffu));
+      for (int f = 0; f < FN + FM; ++f) sf[f] = scale_of((sc[f] >> (8 * B)) & 0xff);
 #pragma unroll
       for (int e = 0; e < 8; e += 2) {
         u32x4_t wb[FN], wa[FM];
@@ -141,51 +163,70 @@ __global__ __launch_bounds__(64 * WGM * WGN) void matmul8_tile_kernel(Matmul8Arg
 #pragma unroll
           for (int j = 0; j < FM; ++j) mma<bf16_t>(acc[i][j], wb[i], wa[j]);
       }
-      return;
-    }
-#pragma unroll
-    for (int i = 0; i < FN; ++i)
-#pragma unroll
-      for (int j = 0; j < FM; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-            fb[slot][i], fa[slot][j], acc[i][j], 0, 0, 0, (int)sc[i], 0, (int)sc[FN + j]);
-  };
-  // The waves meet once the second substep's operands are in registers; the
-  // k-tile after next then goes into the stage just finished.
-  auto ktile = [&](int kt, u32x4_t* cur, const u32x4_t* nxt) {
-    fload(cur, 1, 1);
-    mfmas(0);
-    wait_vm_lgkm0();
-    barrier_no_fence();
-    issue(kt + 2 < nk ? kt + 2 : nk - 1, cur);
-    fload(nxt, 0, 0);
-    mfmas(1);
-    if ((kt & 3) == 3) {
-      const int word = (kt >> 2) + 2;
-#pragma unroll
-      for (int f = 0; f < FN + FM; ++f) {
-        sc[f] = sc_next[f];
-        sc_next[f] = ps[f][word < last_word ? word : last_word];
-      }
     } else {
 #pragma unroll
-      for (int f = 0; f < FN + FM; ++f) sc[f] >>= 8;
+      for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+              fb[slot][i], fa[slot][j], acc[i][j], 0, 0, B, sc[i], B, sc[FN + j]);
     }
   };
+  // the order of one substep: per MFMA two LDS reads and LD / NM loads
+  auto pin = [&](auto loads) __attribute__((always_inline)) {
+    constexpr int LD = decltype(loads)::value, NR = 2 * (FN + FM), NM = FN * FM;
+    if constexpr (!EXACT)
+      static_for<NM>([&](auto x) {
+        constexpr int i = decltype(x)::value;
+        constexpr int r0 = 2 * i < NR ? 2 * i : NR, r = i == NM - 1 ? NR : 2 * i + 2;
+        constexpr int reads = (r < NR ? r : NR) - r0, lds = LD * (i + 1) / NM - LD * i / NM;
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if constexpr (reads > 0) __builtin_amdgcn_sched_group_barrier(0x100, reads, 0);
+        if constexpr (lds > 0) __builtin_amdgcn_sched_group_barrier(0x020, lds, 0);
+      });
+  };
+  // k-tile kt, its scales in byte kt % 4.  The waves meet once the second
+  // substep's operands are in registers; the k-tile after next then goes into
+  // the stage just finished.
+  auto ktile = [&](int kt, u32x4_t* cur, const u32x4_t* nxt, auto byte)
+                   __attribute__((always_inline)) {
+    fload(cur, 1, 1);
+    mfmas(0, byte);
+    pin(std::integral_constant<int, 0>{});
+    __builtin_amdgcn_s_setprio(0);
+    wait_vm_lgkm0();
+    barrier_no_fence();
+    __builtin_amdgcn_s_setprio(1);
+    issue(kt + 2 < nk ? kt + 2 : nk - 1, cur);
+    fload(nxt, 0, 0);
+    mfmas(1, byte);
+    pin(std::integral_constant<int, DPW>{});
+  };
+  // k-tiles 4 w .. 4 w + count - 1; the next four's scales go to Cn.  They
+  // are read after the waits of at least one k-tile's barrier.
+  auto four = [&](int w, int count, const unsigned* C, unsigned* Cn)
+                  __attribute__((always_inline)) {
+    sload(C);
+    issue_scales(w + 1, Cn);
+    ktile(4 * w, S0, S1, std::integral_constant<int, 0>{});
+    if (count > 1) ktile(4 * w + 1, S1, S0, std::integral_constant<int, 1>{});
+    if (count > 2) ktile(4 * w + 2, S0, S1, std::integral_constant<int, 2>{});
+    if (count > 3) ktile(4 * w + 3, S1, S0, std::integral_constant<int, 3>{});
+  };
+  issue_scales(0, C0);
   issue(0, S0);
-#pragma unroll
-  for (int f = 0; f < FN + FM; ++f) {
-    sc[f] = ps[f][0];
-    sc_next[f] = ps[f][last_word < 1 ? last_word : 1];
-  }
   wait_vmcnt<0>();
   barrier_no_fence();
   issue(nk > 1 ? 1 : 0, S1);
   fload(S0, 0, 0);
-  for (int kt = 0; kt < nk; kt += 2) {
-    ktile(kt, S0, S1);
-    if (kt + 1 < nk) ktile(kt + 1, S1, S0);
+  int w = 0;
+  for (; 4 * w + 8 <= nk; w += 2) {
+    four(w, 4, C0, C1);
+    four(w + 1, 4, C1, C0);
   }
+  const int left = nk - 4 * w;  // 0 .. 7
+  if (left > 0) four(w, left, C0, C1);
+  if (left > 4) four(w + 1, left - 4, C1, C0);
   wait_vmcnt<0>();
   __syncthreads();
 
@@ -226,7 +267,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void matmul8_tile_kernel(Matmul8Arg
           v[4 + e] = hi[e];
         }
         const int m = m0 + wm * WTM + j * 32 + rr, n = n0 + wn * WTN + h * HC + 8 * c;
-        if (m < g.m) store8_edge(y + (long long)m * g.ldy + n, g.n - n, v);
+        if (m < g.m) store8_edge<STRM>(y + (long long)m * g.ldy + n, g.n - n, v);
       }
       asm volatile("" ::: "memory");
     }
@@ -307,9 +348,26 @@ __global__ __launch_bounds__(64 * kFewWaves) void matmul8_rows_kernel(Matmul8Arg
 }
 
 namespace {
+template <int BM, int BN, int WGM, int WGN, typename Y>
+void tiles(Matmul8Args a, hipStream_t s) {
+  constexpr bool EXACT = std::is_same_v<Y, float>;
+  a.tiles_m = (a.m + BM - 1) / BM;
+  a.tiles_n = (a.n + BN - 1) / BN;
+  // tiles of a column that run side by side on an XCD's 32 CUs
+  a.group_m = 6;
+  const dim3 grid((unsigned)a.tiles_m * (unsigned)a.tiles_n), block(64 * WGM * WGN);
+  // A result larger than the last-level cache is stored past it, which leaves
+  // the cache to the operands (16384 x 16384 x 4096, 512 MB: 911 -> 882 us); a
+  // smaller one stays there for its reader (8192 x 4096, 64 MB: 108 us, 113
+  // stored past).
+  if ((double)a.m * a.n * sizeof(Y) > 256.0 * (1 << 20))
+    hipLaunchKernelGGL((matmul8_tile_kernel<BM, BN, WGM, WGN, EXACT, true, Y>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((matmul8_tile_kernel<BM, BN, WGM, WGN, EXACT, false, Y>), grid, block, 0, s, a);
+}
+
 template <typename Y>
-void go(const Matmul8Args& in, hipStream_t s) {
-  Matmul8Args a = in;
+void go(const Matmul8Args& a, hipStream_t s) {
   if (a.m <= kFewRows) {
     const dim3 grid((a.n + 15) / 16), block(64 * kFewWaves);
     if (a.m <= 16)
@@ -320,23 +378,13 @@ void go(const Matmul8Args& in, hipStream_t s) {
       hipLaunchKernelGGL((matmul8_rows_kernel<4, Y>), grid, block, 0, s, a);
     return;
   }
-  auto tiles = [&](int bm, int bn) {
-    a.tiles_m = (a.m + bm - 1) / bm;
-    a.tiles_n = (a.n + bn - 1) / bn;
-    a.group_m = 8;
-    return (long long)a.tiles_m * a.tiles_n;
-  };
   if constexpr (std::is_same_v<Y, float>) {
-    tiles(128, 128);
-    hipLaunchKernelGGL((matmul8_tile_kernel<128, 128, 2, 2, true, Y>),
-                       dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(256), 0, s, a);
-  } else if (tiles(256, 256) >= 256) {
-    hipLaunchKernelGGL((matmul8_tile_kernel<256, 256, 4, 2, false, Y>),
-                       dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(512), 0, s, a);
+    tiles<128, 128, 2, 2, Y>(a, s);
   } else {
-    tiles(128, 128);
-    hipLaunchKernelGGL((matmul8_tile_kernel<128, 128, 2, 2, false, Y>),
-                       dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(256), 0, s, a);
+    if ((long long)((a.m + 255) / 256) * ((a.n + 255) / 256) >= 256)
+      tiles<256, 256, 4, 2, Y>(a, s);
+    else
+      tiles<128, 128, 2, 2, Y>(a, s);
   }
 }
 }  // namespace

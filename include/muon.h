@@ -296,8 +296,8 @@ int muon_matmul8(const muon_tensor8* a, const muon_tensor8* b, void* y, int y_dt
 
 /* dw = dy^T x, or with accumulate dw += dy^T x: the gradient of W (n x k,
  * dense, as muon_step takes it) from the layer's output gradient dy (tokens x
- * n, bf16; fp32 returns MUON_ERR_UNSUPPORTED) and its input x (tokens x k) kept
- * in 8 bits.  Sums in fp32.  dw is fp32 or bf16; accumulating into bf16
+ * n, bf16, lddy <= 2^26; fp32 and longer strides return MUON_ERR_UNSUPPORTED)
+ * and its input x (tokens x k) kept in 8 bits.  Sums in fp32.  dw is fp32 or bf16; accumulating into bf16
  * returns MUON_ERR_UNSUPPORTED (every addition would be rounded to 8 bits of
  * mantissa).  The workspace (muon_weight_grad_workspace_bytes, possibly 0, then
  * it may be NULL) holds partial sums. */

@@ -170,8 +170,7 @@ int muon_matmul8(const muon_tensor8* a, const muon_tensor8* b, void* y, int y_dt
 
 size_t muon_weight_grad_workspace_bytes(int tokens, int n, int k) {
   if (tokens < 0 || n < 1 || k < 1) return 0;
-  int per;
-  const int splits = weight_grad_splits(tokens, n, k, &per);
+  const int splits = weight_grad_plan(tokens, n, k).splits;
   return splits > 1 ? (size_t)splits * (size_t)n * (size_t)k * sizeof(float) : 0;
 }
 
@@ -186,7 +185,9 @@ int muon_weight_grad(const void* dy, int dy_dtype, long long lddy, int tokens, i
   const Span out = matrix(dw, n, x->cols, x->cols, size_of(dw_dtype));
   const Span in = matrix(dy, tokens, n, lddy, size_of(dy_dtype));
   if (conflict({out}, {in, data_of(x), scale_of(x)})) return MUON_ERR_INVALID_ARG;
-  if (dy_dtype != MUON_BF16 || (accumulate && dw_dtype != MUON_FP32) || !tiles_fit(n, x->cols))
+  // (the kernel reaches the rows of a tile with 32-bit offsets)
+  if (dy_dtype != MUON_BF16 || (accumulate && dw_dtype != MUON_FP32) || !tiles_fit(n, x->cols) ||
+      lddy > (1LL << 26))
     return MUON_ERR_UNSUPPORTED;
   const size_t need = muon_weight_grad_workspace_bytes(tokens, n, x->cols);
   if (need) {
@@ -203,13 +204,13 @@ int muon_weight_grad(const void* dy, int dy_dtype, long long lddy, int tokens, i
   g.tokens = tokens; g.n = n; g.k = x->cols;
   g.ld = (int)ld8(x->cols); g.sld = (int)scale_ld8(x->cols); g.shift = shift_of(x);
   g.dw = dw; g.accumulate = accumulate;
-  g.splits = weight_grad_splits(tokens, n, x->cols, &g.tiles_per_split);
+  const WeightGradPlan plan = weight_grad_plan(tokens, n, x->cols);
   g.part = need ? static_cast<float*>(workspace) : nullptr;
   const double t = tokens, k = x->cols;
   return status_of(timed_launch(
       MUON_K_WEIGHT_GRAD, n, x->cols, 2 * t * n * k, 2 * t * n * k,
       2 * t * n + t * k + n * k * size_of(dw_dtype) * (accumulate ? 2 : 1), stream,
-      [&] { return launch_weight_grad(dw_dtype == MUON_BF16, g, stream); }));
+      [&] { return launch_weight_grad(dw_dtype == MUON_BF16, g, plan, stream); }));
 }
 
 int muon_layer_norm(const void* x, int x_dtype, long long ldx, int rows, int cols,

@@ -73,8 +73,13 @@ struct WeightGradArgs {
   int splits, tiles_per_split;  // token tiles of a split
   int tiles_n, tiles_k;
 };
-int weight_grad_splits(int tokens, int n, int k, int* tiles_per_split);
-hipError_t launch_weight_grad(int dw_bf16, const WeightGradArgs& a, hipStream_t s);
+struct WeightGradPlan {
+  int kind, splits, tiles_per_split;  // tile variant; token splits, token tiles in each
+  int bn, bk;
+};
+WeightGradPlan weight_grad_plan(int tokens, int n, int k);
+hipError_t launch_weight_grad(int dw_bf16, const WeightGradArgs& a, const WeightGradPlan& p,
+                              hipStream_t s);
 
 struct NormArgs {
   const void* x;

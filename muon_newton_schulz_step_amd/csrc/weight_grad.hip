@@ -20,6 +20,30 @@ namespace muon {
 
 constexpr int kTileT = 64;  // tokens per LDS tile
 
+// Wait until this wave has no LDS operation in flight (lgkmcnt(0), the other
+// counters untouched: loads into registers stay in flight).
+__device__ __forceinline__ void wait_lgkm0() {
+#if defined(__HIP_DEVICE_COMPILE__)
+  __builtin_amdgcn_s_waitcnt(0xc07f);
+#endif
+}
+
+// A workgroup computes a BN x BK tile of dw in WGN x WGK waves of 32x32 MFMA
+// tiles.  A token tile of both operands lies in LDS as bf16 rows [t][column]
+// (64-byte segments permuted by t % 4 as for the step's row-major operand, so
+// that the 4 rows of a transposing read fall on 4 quarters of the bank line),
+// two stages.  Loads go through registers, because x changes its type on the
+// way and because rows of any stride and a ragged last tile then go the same
+// way.  While token tile kt is multiplied, kt + 1 goes from registers to the
+// other stage in the first of the four substeps of 16 tokens, and the loads of
+// kt + 2 follow at once: they have three quarters of a tile and its barrier to
+// arrive.  The waves meet before the last substep, whose operands are in
+// registers by then, and read the next tile's first ones during it.  After each
+// MFMA comes its share of the substep's LDS reads and writes.
+//   8192 tokens, 4096 x 4096, 256 x 256 tiles: 232 us, 1.19 PFLOP/s (393 us
+//   with 128 x 128 tiles on 4 waves, everything loaded and stored at the tile's
+//   ends, and no order pinned; a library's plain bf16 product runs at 1.41).
+
 template <int BN, int BK, int WGN, int WGK, typename W>
 __global__ __launch_bounds__(64 * WGN * WGK) void weight_grad_kernel(WeightGradArgs g) {
   constexpr int NT = 64 * WGN * WGK;
@@ -28,7 +52,9 @@ __global__ __launch_bounds__(64 * WGN * WGK) void weight_grad_kernel(WeightGradA
   constexpr int UN = BN / 8, UK = BK / 8;          // chunks of 8 per token row
   constexpr int PN = kTileT * UN / NT, PK = kTileT * UK / NT;
   static_assert(PN * NT == kTileT * UN && PK * NT == kTileT * UK, "chunks split over the threads");
-  __shared__ u32x4_t lds[2][kTileT * (UN + UK)];
+  static_assert(NT % UN == 0 && NT % UK == 0, "a thread keeps its columns");
+  constexpr int SN = kTileT * UN, SK = kTileT * UK;
+  __shared__ u32x4_t Ln[2 * SN], Lk[2 * SK];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wn = wave / WGK, wk = wave % WGK;
@@ -40,47 +66,61 @@ __global__ __launch_bounds__(64 * WGN * WGK) void weight_grad_kernel(WeightGradA
   const int t_all = (g.tokens + kTileT - 1) / kTileT;
   const int t_end = t_first + g.tiles_per_split < t_all ? t_first + g.tiles_per_split : t_all;
 
+  // the thread's chunks: columns cn (of dy) and ck (of x), rows tn + i NT / UN
+  // and tk + i NT / UK
+  const int tn = tid / UN, cn = tid % UN, tk = tid / UK, ck = tid % UK;
+  const int n = n0 + 8 * cn, k = k0 + 8 * ck;
+  const bool k_in = k < g.ld, n_all = n0 + BN <= g.n;
+  const unsigned dy_off = (unsigned)tn * (unsigned)g.lddy + (n < g.n ? 8 * cn : 0);
+  const unsigned x_off = (unsigned)tk * (unsigned)g.ld + (k_in ? 8 * ck : 0);
+  const unsigned s_off = (g.shift ? 0u : (unsigned)tk * (unsigned)g.sld) + (k_in ? ck >> 4 : 0);
   u32x4_t rd[PN];
   u32x2_t rx[PK];
   int sx[PK];
-  auto gload = [&](int kt) {
+  // A chunk past dy's or x's last column reads the tile's first one, and one
+  // across dy's last column reads into the next row: what comes of them is not
+  // stored.  Only the last row has no next one, and rows past it must be zero:
+  // the last token tile is loaded element by element where that matters.
+  auto gload = [&](int kt) __attribute__((always_inline)) {
+    const int t0 = kt * kTileT;
+    const bool all = t0 + kTileT <= g.tokens;
+    const bf16_t* dyb = static_cast<const bf16_t*>(g.dy) + (long long)t0 * g.lddy + n0;
+    const unsigned char* xb = g.x + (long long)t0 * g.ld + k0;
+    const unsigned char* sb = g.sx + (long long)(t0 >> g.shift) * g.sld + (k0 >> 7);
+    if (n_all ? all : t0 + kTileT < g.tokens) {
 #pragma unroll
-    for (int i = 0; i < PN; ++i) {
-      const int q = tid + NT * i, t = kt * kTileT + q / UN, n = n0 + q % UN * 8;
-      const bf16_t* p = static_cast<const bf16_t*>(g.dy) + (long long)t * g.lddy + n;
-      rd[i] = u32x4_t{0u, 0u, 0u, 0u};
-      if (t < g.tokens) {
-        if (n + 8 <= g.n) {
-          __builtin_memcpy(&rd[i], p, 16);
-        } else {
-          float v[8];
-          load8_edge(p, g.n - n, v);
+      for (int i = 0; i < PN; ++i)
+        __builtin_memcpy(&rd[i], dyb + (long long)(NT / UN * i) * g.lddy + dy_off, 16);
+    } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) rd[i][e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-        }
+      for (int i = 0; i < PN; ++i) {
+        float v[8];
+        load8_edge(dyb + (long long)(NT / UN * i) * g.lddy + dy_off,
+                   t0 + tn + NT / UN * i < g.tokens ? g.n - n : 0, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rd[i][e] = pack_bf16(v[2 * e], v[2 * e + 1]);
       }
     }
 #pragma unroll
     for (int i = 0; i < PK; ++i) {
-      const int q = tid + NT * i, t = kt * kTileT + q / UK, k = k0 + q % UK * 8;
       rx[i] = u32x2_t{0u, 0u};
       sx[i] = 127;
-      if (t < g.tokens && k < g.ld) {
-        rx[i] = *reinterpret_cast<const u32x2_t*>(g.x + (long long)t * g.ld + k);
-        sx[i] = g.sx[(long long)(t >> g.shift) * g.sld + (k >> 7)];
+      if (all || t0 + tk + NT / UK * i < g.tokens) {
+        rx[i] = *reinterpret_cast<const u32x2_t*>(xb + (long long)(NT / UK * i) * g.ld + x_off);
+        sx[i] = sb[(g.shift ? 0 : (long long)(NT / UK * i) * g.sld) + s_off];
       }
     }
   };
-  auto lstore = [&](u32x4_t* St) {
+  auto lstore = [&](int st) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < PN; ++i) {
-      const int q = tid + NT * i, t = q / UN;
-      St[t * UN + qrow_unit<BN / 32>(t, q % UN)] = rd[i];
+      const int t = tn + NT / UN * i;
+      Ln[st * SN + t * UN + qrow_unit<4>(t, cn)] = rd[i];
     }
 #pragma unroll
     for (int i = 0; i < PK; ++i) {
-      const int q = tid + NT * i, t = q / UK;
-      St[kTileT * UN + t * UK + qrow_unit<BK / 32>(t, q % UK)] =
+      const int t = tk + NT / UK * i;
+      Lk[st * SK + t * UK + qrow_unit<4>(t, ck)] =
           bf16_of_e4m3(rx[i][0], rx[i][1], scale_of(sx[i]));
     }
   };
@@ -97,44 +137,82 @@ __global__ __launch_bounds__(64 * WGN * WGK) void weight_grad_kernel(WeightGradA
   const int hsel = lane >> 5;
   const int tr_k = 8 * hsel + ((lane & 15) >> 2);
   const int tr_j = 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+  u32x4_t fn[2][FN], fk[2][FK];
   auto frag = [&](const u32x4_t* P, auto units, int kk, int j) __attribute__((always_inline)) {
     constexpr int U = decltype(units)::value;
     u32x2_t h[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int k = 16 * kk + tr_k + 4 * s;
+      const int kr = 16 * kk + tr_k + 4 * s;
       h[s] = lds_read_tr16(reinterpret_cast<const unsigned char*>(P) +
-                           (k * U + qrow_unit<U / 4>(k, j >> 3)) * 16 + (j & 7) * 2);
+                           (kr * U + qrow_unit<4>(kr, j >> 3)) * 16 + (j & 7) * 2);
     }
     return u32x4_t{h[0][0], h[0][1], h[1][0], h[1][1]};
   };
-  auto compute = [&](const u32x4_t* St) {
+  auto fload = [&](int st, int kk, int slot) __attribute__((always_inline)) {
+    auto rn = [&](int i) __attribute__((always_inline)) {
+      fn[slot][i] = frag(Ln + st * SN, std::integral_constant<int, UN>{}, kk, wn * WTN + 32 * i + tr_j);
+    };
+    rn(0);
 #pragma unroll
-    for (int kk = 0; kk < kTileT / 16; ++kk) {
-      u32x4_t fn[FN], fk[FK];
+    for (int j = 0; j < FK; ++j)
+      fk[slot][j] = frag(Lk + st * SK, std::integral_constant<int, UK>{}, kk,
+                         wk * WTK + 32 * j + tr_j);
 #pragma unroll
-      for (int i = 0; i < FN; ++i)
-        fn[i] = frag(St, std::integral_constant<int, UN>{}, kk, wn * WTN + 32 * i + tr_j);
+    for (int i = 1; i < FN; ++i) rn(i);
+  };
+  auto mfmas = [&](int slot) __attribute__((always_inline)) {
 #pragma unroll
-      for (int j = 0; j < FK; ++j)
-        fk[j] = frag(St + kTileT * UN, std::integral_constant<int, UK>{}, kk,
-                     wk * WTK + 32 * j + tr_j);
+    for (int i = 0; i < FN; ++i)
 #pragma unroll
-      for (int i = 0; i < FN; ++i)
-#pragma unroll
-        for (int j = 0; j < FK; ++j) mma<bf16_t>(acc[i][j], fn[i], fk[j]);
-    }
+      for (int j = 0; j < FK; ++j) mma<bf16_t>(acc[i][j], fn[slot][i], fk[slot][j]);
+  };
+  // one substep's order: after each MFMA its share of the LDS reads, of WR LDS
+  // writes and of LD loads
+  auto pins = [&](auto wr, auto ld) __attribute__((always_inline)) {
+    constexpr int WR = decltype(wr)::value, LD = decltype(ld)::value;
+    constexpr int NR = 2 * (FN + FK), NM = FN * FK;
+    static_for<NM>([&](auto x) {
+      constexpr int i = decltype(x)::value;
+      constexpr int rd_ = NR * (i + 1) / NM - NR * i / NM, w_ = WR * (i + 1) / NM - WR * i / NM,
+                    l_ = LD * (i + 1) / NM - LD * i / NM;
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if constexpr (rd_ > 0) __builtin_amdgcn_sched_group_barrier(0x100, rd_, 0);
+      if constexpr (w_ > 0) __builtin_amdgcn_sched_group_barrier(0x200, w_, 0);
+      if constexpr (l_ > 0) __builtin_amdgcn_sched_group_barrier(0x020, l_, 0);
+    });
+  };
+  using Z = std::integral_constant<int, 0>;
+  auto ttile = [&](int kt, int cur, int nxt) __attribute__((always_inline)) {
+    lstore(nxt);
+    fload(cur, 1, 1);
+    mfmas(0);
+    pins(std::integral_constant<int, PN + PK>{}, Z{});
+    if (kt + 2 < t_end) gload(kt + 2);
+    fload(cur, 2, 0);
+    mfmas(1);
+    pins(Z{}, Z{});
+    fload(cur, 3, 1);
+    mfmas(0);
+    pins(Z{}, Z{});
+    __builtin_amdgcn_s_setprio(0);
+    wait_lgkm0();
+    barrier_no_fence();
+    __builtin_amdgcn_s_setprio(1);
+    fload(nxt, 0, 0);
+    mfmas(1);
+    pins(Z{}, Z{});
   };
   if (t_first < t_end) {
     gload(t_first);
-    lstore(lds[0]);
-    __syncthreads();
-    for (int kt = t_first; kt < t_end; ++kt) {
-      const int cur = (kt - t_first) & 1;
-      if (kt + 1 < t_end) gload(kt + 1);
-      compute(lds[cur]);
-      if (kt + 1 < t_end) lstore(lds[cur ^ 1]);
-      __syncthreads();
+    lstore(0);
+    if (t_first + 1 < t_end) gload(t_first + 1);
+    wait_lgkm0();
+    barrier_no_fence();
+    fload(0, 0, 0);
+    for (int kt = t_first; kt < t_end; kt += 2) {
+      ttile(kt, 0, 1);
+      if (kt + 1 < t_end) ttile(kt + 1, 1, 0);
     }
   }
 
@@ -189,27 +267,61 @@ __global__ __launch_bounds__(256) void weight_grad_join_kernel(const float* part
     if (e < n) w[e] = from_f32<W>(accumulate ? to_f32(w[e]) + s[e] : s[e]);
 }
 
-// Token splits: enough workgroups for two per CU, and at least four token
-// tiles in each.
-int weight_grad_splits(int tokens, int n, int k, int* tiles_per_split) {
-  const long long tiles = (long long)((n + 127) / 128) * ((k + 127) / 128);
-  const int tt = (tokens + kTileT - 1) / kTileT;
-  long long want = 512 / tiles;
-  if (want > tt / 4) want = tt / 4;
-  if (want < 1) want = 1;
-  const int per = tt > 0 ? (int)((tt + want - 1) / want) : 1;
-  *tiles_per_split = per;
-  return tt > 0 ? (tt + per - 1) / per : 1;
+// The tile and the number of token splits.  A CU holds one workgroup of 256 x
+// 256 or 256 x 128 tiles, or two of 128 x 128 ones, all of 8 waves.  Measured per
+// token tile: 1.78 us (256 x 256), 1.15 us (256 x 128), and for 128 x 128
+// 0.78 us alone on its CU, 1.3 us for two.  The result and its parts move at
+// about 4.7 TB/s, written and read, and a second launch costs about 3 us.  The
+// plan takes the smallest sum.  (4096 tokens, 1280 x 5120: 104 us, 72 us,
+// 78 us with the three tiles; 16384 tokens, 768 x 1024, in 10 parts: 56, 41,
+// 44 us; 8192 tokens, 4096 x 4096: 232, 288, 333 us.)
+WeightGradPlan weight_grad_plan(int tokens, int n, int k) {
+  struct Kind {
+    int bn, bk, per_cu;
+    double one, full;  // us per token tile: alone on its CU, all places taken
+  };
+  static const Kind kinds[3] = {
+      {256, 256, 1, 1.78, 1.78}, {256, 128, 1, 1.15, 1.15}, {128, 128, 2, 0.78, 1.3}};
+  const int tt = (int)(((long long)tokens + kTileT - 1) / kTileT);
+  WeightGradPlan best{};
+  double least = 0.0;
+  for (int i = 0; i < 3; ++i) {
+    const Kind& c = kinds[i];
+    const long long tiles = (long long)((n + c.bn - 1) / c.bn) * ((k + c.bk - 1) / c.bk);
+    for (int want = 1; want <= 64; ++want) {
+      // at least four token tiles in a part, and no more parts than fill the chip
+      if (want > 1 && (want > tt / 4 || tiles * (want - 1) >= 256 * c.per_cu)) break;
+      const int per = tt > 0 ? (tt + want - 1) / want : 1;
+      const int splits = tt > 0 ? (tt + per - 1) / per : 1;
+      const long long wgs = tiles * splits;
+      const double us_tile = wgs <= 256 ? c.one : c.full;
+      const double rounds = (double)((wgs + 256 * c.per_cu - 1) / (256 * c.per_cu));
+      double us = rounds * per * us_tile;
+      if (splits > 1) us += 3.0 + 2.0 * splits * 4.0 * n * k / 4.7e6;
+      if (best.splits == 0 || us < least) {
+        least = us;
+        best = WeightGradPlan{i, splits, per, c.bn, c.bk};
+      }
+    }
+  }
+  return best;
 }
 
 namespace {
 template <typename W>
-void go(const WeightGradArgs& in, hipStream_t s) {
+void go(const WeightGradArgs& in, const WeightGradPlan& p, hipStream_t s) {
   WeightGradArgs a = in;
-  a.tiles_n = (a.n + 127) / 128;
-  a.tiles_k = (a.k + 127) / 128;
-  hipLaunchKernelGGL((weight_grad_kernel<128, 128, 2, 2, W>),
-                     dim3((unsigned)(a.tiles_n * a.tiles_k * a.splits)), dim3(256), 0, s, a);
+  a.splits = p.splits;
+  a.tiles_per_split = p.tiles_per_split;
+  a.tiles_n = (a.n + p.bn - 1) / p.bn;
+  a.tiles_k = (a.k + p.bk - 1) / p.bk;
+  const dim3 grid((unsigned)a.tiles_n * (unsigned)a.tiles_k * (unsigned)a.splits), block(512);
+  if (p.kind == 0)
+    hipLaunchKernelGGL((weight_grad_kernel<256, 256, 2, 4, W>), grid, block, 0, s, a);
+  else if (p.kind == 1)
+    hipLaunchKernelGGL((weight_grad_kernel<256, 128, 4, 2, W>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((weight_grad_kernel<128, 128, 2, 4, W>), grid, block, 0, s, a);
   if (a.part) {
     const long long elems = (long long)a.n * a.k;
     hipLaunchKernelGGL(weight_grad_join_kernel<W>, dim3((unsigned)((elems + 1023) / 1024)),
@@ -218,11 +330,12 @@ void go(const WeightGradArgs& in, hipStream_t s) {
 }
 }  // namespace
 
-hipError_t launch_weight_grad(int dw_bf16, const WeightGradArgs& a, hipStream_t s) {
+hipError_t launch_weight_grad(int dw_bf16, const WeightGradArgs& a, const WeightGradPlan& p,
+                              hipStream_t s) {
   if (dw_bf16)
-    go<bf16_t>(a, s);
+    go<bf16_t>(a, p, s);
   else
-    go<float>(a, s);
+    go<float>(a, p, s);
   return hipGetLastError();
 }
 

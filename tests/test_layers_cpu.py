@@ -92,6 +92,7 @@ def weight_grad(dy=P, dy_dtype=BF16, lddy=48, tokens=8, n=48, x=None, dw=P * 2, 
 @pytest.mark.parametrize("kw,expect", [
     (dict(dy_dtype=3), INVALID), (dict(dw_dtype=3), INVALID), (dict(accumulate=2), INVALID),
     (dict(dy_dtype=FP32), UNSUPPORTED), (dict(dw_dtype=BF16, accumulate=1), UNSUPPORTED),
+    (dict(lddy=(1 << 26) + 1, tokens=1, x=t8(1, 1), dy=P << 20), UNSUPPORTED),
     (dict(dy=0), INVALID), (dict(lddy=47), INVALID), (dict(n=0), INVALID), (dict(tokens=7), INVALID),
     (dict(tokens=-1, x=t8(1, rows=-1)), INVALID), (dict(dw=0), INVALID), (dict(dw=P + 16), INVALID),
     (dict(dw=P * 64 + 128), INVALID), (dict(x=t8(1, data=P * 64 + 4)), INVALID),

@@ -167,12 +167,57 @@ __device__ __forceinline__ unsigned max16(unsigned u) {
   return u;
 }
 
-// Sum over the wave, the same in all lanes and from run to run.
+// Sum over the wave, the same in all lanes and from run to run: DPP adds inside
+// rows of 16 lanes, then across the rows; lane 63 ends up with the total.
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-  return v;
+  auto add = [&](auto ctrl, auto rows) __attribute__((always_inline)) {
+    v += __uint_as_float((unsigned)__builtin_amdgcn_update_dpp(
+        0, (int)__float_as_uint(v), decltype(ctrl)::value, decltype(rows)::value, 0xf, false));
+  };
+  using All = std::integral_constant<int, 0xf>;
+  add(std::integral_constant<int, 0x111>{}, All{});  // row_shr:1
+  add(std::integral_constant<int, 0x112>{}, All{});
+  add(std::integral_constant<int, 0x114>{}, All{});
+  add(std::integral_constant<int, 0x118>{}, All{});
+  add(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xa>{});  // row_bcast:15
+  add(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xc>{});  // row_bcast:31
+  return __uint_as_float((unsigned)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
+
+// Eight consecutive elements as they lie in memory, so that a row can be on
+// its way while another one is worked on.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<bf16_t> {
+  u32x4_t w;
+  __device__ __forceinline__ void load(const bf16_t* p, int n) {
+    if (n >= 8) {
+      __builtin_memcpy(&w, p, 16);
+    } else {
+      float v[8];
+      load8_edge(p, n, v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Raw8<float> {
+  float w[8];
+  __device__ __forceinline__ void load(const float* p, int n) { load8_edge(p, n, w); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = w[i];
+  }
+};
 
 // The four scale bytes of a wave whose rows of 16 lanes each hold one, as a
 // word (the same in all lanes).

@@ -43,6 +43,8 @@ __device__ __forceinline__ void team_sum(float (&v)[N], float (*buf)[16], int wa
   }
 }
 
+// Rows beyond the last one: a team without a row still takes part in the
+// workgroup's barriers.
 template <int XT, int OUT, int TEAM, int NCH>
 __global__ __launch_bounds__(TEAM > 4 ? 64 * TEAM : 256) void layer_norm_kernel(NormArgs a) {
   using X = typename ElemOf<XT>::type;
@@ -61,16 +63,24 @@ __global__ __launch_bounds__(TEAM > 4 ? 64 * TEAM : 256) void layer_norm_kernel(
     load8_edge(a.bias ? a.bias + col[k] : nullptr, a.bias ? a.cols - col[k] : 0, b[k]);
   }
   const float n = (float)a.cols;
-  for (long long row = (long long)blockIdx.x * TEAMS + wave / TEAM; row < a.rows; row += step) {
-    float x[NCH][8];
+  Raw8<X> raw[NCH];
+  auto fetch = [&](long long row) __attribute__((always_inline)) {
     const X* xr = static_cast<const X*>(a.x) + row * a.ldx;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) raw[k].load(xr + col[k], a.cols - col[k]);
+  };
+  long long row = (long long)blockIdx.x * TEAMS + wave / TEAM;
+  if (row < a.rows) fetch(row);
+  for (; row < a.rows; row += step) {
+    float x[NCH][8];
     float s[1] = {0.f};
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
-      load8_edge(xr + col[k], a.cols - col[k], x[k]);
+      raw[k].get(x[k]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[0] += x[k][i];
     }
+    if (row + step < a.rows) fetch(row + step);
     team_sum<TEAM>(s, sums[0], tw, lane);
     const float mu = s[0] / n;  // exact for a row of equal values
     s[0] = 0.f;
@@ -116,15 +126,40 @@ __global__ __launch_bounds__(TEAM > 4 ? 64 * TEAM : 256) void layer_norm_kernel(
   }
 }
 
+// The input of the backward pass: eight elements of a row of x, from memory
+// or from the 8-bit tensor.
+template <int XT>
+struct RawX {
+  Raw8<typename ElemOf<XT>::type> r;
+  __device__ __forceinline__ void load(const NormBackArgs& a, long long row, int col) {
+    r.load(static_cast<const typename ElemOf<XT>::type*>(a.x) + row * a.ldx + col, a.cols - col);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { r.get(v); }
+};
+template <>
+struct RawX<kOut8> {
+  u32x2_t q;
+  int byte;
+  __device__ __forceinline__ void load(const NormBackArgs& a, long long row, int col) {
+    q = u32x2_t{0u, 0u};
+    byte = 127;
+    if (col < a.ld) {
+      q = *reinterpret_cast<const u32x2_t*>(a.x8 + row * a.ld + col);
+      byte = a.sx8[(row >> a.shift) * a.sld + (col >> 7)];
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { from_e4m3(q, scale_of(byte), v); }
+};
+
+constexpr int back_waves(int team) { return team > 8 ? team : 8; }
+
 template <int DT, int XT, int TEAM, int NCH>
-__global__ __launch_bounds__(TEAM > 4 ? 64 * TEAM : 256) void layer_norm_back_kernel(
-    NormBackArgs a) {
+__global__ __launch_bounds__(64 * back_waves(TEAM)) void layer_norm_back_kernel(NormBackArgs a) {
   using D = typename ElemOf<DT>::type;
-  using X = typename ElemOf<XT>::type;
-  constexpr int WAVES = TEAM > 4 ? TEAM : 4, TEAMS = WAVES / TEAM;
-  __shared__ float sums[2][2][16];
+  constexpr int WAVES = back_waves(TEAM), TEAMS = WAVES / TEAM;
+  __shared__ float sums[2][TEAMS][2][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int tw = wave % TEAM;
+  const int tw = wave % TEAM, team = wave / TEAM;
   const long long step = (long long)gridDim.x * TEAMS;
   int col[NCH];
   float w[NCH][8], dw[NCH][8], db[NCH][8];
@@ -136,71 +171,87 @@ __global__ __launch_bounds__(TEAM > 4 ? 64 * TEAM : 256) void layer_norm_back_ke
     for (int i = 0; i < 8; ++i) dw[k][i] = db[k][i] = 0.f;
   }
   const float n = (float)a.cols;
-  int turn = 0;
-  for (long long row = (long long)blockIdx.x * TEAMS + wave / TEAM; row < a.rows; row += step) {
-    float x[NCH][8], d[NCH][8];
-    const float mu = a.mean[row], r = a.rstd[row];
-    float s[2] = {0.f, 0.f};
+  RawX<XT> rx[NCH];
+  Raw8<D> rd[NCH];
+  float mu_next = 0.f, r_next = 0.f;
+  auto fetch = [&](long long row) __attribute__((always_inline)) {
+    mu_next = a.mean[row];
+    r_next = a.rstd[row];
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
-      if constexpr (XT == kOut8) {
-        u32x2_t q = {0u, 0u};
-        int byte = 127;
-        if (col[k] < a.ld) {
-          q = *reinterpret_cast<const u32x2_t*>(a.x8 + row * a.ld + col[k]);
-          byte = a.sx8[(row >> a.shift) * a.sld + (col[k] >> 7)];
-        }
-        from_e4m3(q, scale_of(byte), x[k]);
-      } else {
-        load8_edge(static_cast<const X*>(a.x) + row * a.ldx + col[k], a.cols - col[k], x[k]);
-      }
-      load8_edge(static_cast<const D*>(a.dy) + row * a.lddy + col[k], a.cols - col[k], d[k]);
+      rx[k].load(a, row, col[k]);
+      rd[k].load(static_cast<const D*>(a.dy) + row * a.lddy + col[k], a.cols - col[k]);
     }
+  };
+  int turn = 0;
+  long long first = (long long)blockIdx.x * TEAMS;  // of the workgroup's teams
+  if (first + team < a.rows) fetch(first + team);
+  for (; first < a.rows; first += step) {
+    const long long row = first + team;
+    const bool in = row < a.rows;
+    float x[NCH][8], d[NCH][8];
+    const float mu = mu_next, r = r_next;
+    float s[2] = {0.f, 0.f};
+    if (in) {
 #pragma unroll
-    for (int k = 0; k < NCH; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        // beyond the last column dy and w are zero, and x has no part
-        const float xh = col[k] + i < a.cols ? (x[k][i] - mu) * r : 0.f;
-        db[k][i] += d[k][i];
-        dw[k][i] = fmaf(d[k][i], xh, dw[k][i]);
-        const float g = d[k][i] * w[k][i];
-        s[0] += g;
-        s[1] = fmaf(g, xh, s[1]);
-        x[k][i] = xh;
-        d[k][i] = g;
+      for (int k = 0; k < NCH; ++k) {
+        rx[k].get(x[k]);
+        rd[k].get(d[k]);
       }
-    team_sum<TEAM>(s, sums[turn], tw, lane);
+      if (row + step < a.rows) fetch(row + step);
+#pragma unroll
+      for (int k = 0; k < NCH; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          // beyond the last column dy and w are zero, and x has no part
+          const float xh = col[k] + i < a.cols ? (x[k][i] - mu) * r : 0.f;
+          db[k][i] += d[k][i];
+          dw[k][i] = fmaf(d[k][i], xh, dw[k][i]);
+          const float g = d[k][i] * w[k][i];
+          s[0] += g;
+          s[1] = fmaf(g, xh, s[1]);
+          x[k][i] = xh;
+          d[k][i] = g;
+        }
+    }
+    team_sum<TEAM>(s, sums[turn][team], tw, lane);
     turn ^= 1;
     const float c0 = s[0] / n, c1 = s[1] / n;
+    if (in) {
 #pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      float o[8];
+      for (int k = 0; k < NCH; ++k) {
+        float o[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = r * (d[k][i] - c0 - x[k][i] * c1);
-      store8_edge(static_cast<D*>(a.dx) + row * a.lddx + col[k], a.cols - col[k], o);
+        for (int i = 0; i < 8; ++i) o[i] = r * (d[k][i] - c0 - x[k][i] * c1);
+        store8_edge(static_cast<D*>(a.dx) + row * a.lddx + col[k], a.cols - col[k], o);
+      }
     }
   }
-  // the workgroup's sums: its teams' one after the other, in their order
+  // the workgroup's sums: every team's go to LDS (element i of a chunk's lanes
+  // side by side, the rows of 64 padded by one, so that neither the writes nor
+  // the reads meet in a bank) and are added in the teams' order
   float* part = a.part + (long long)blockIdx.x * 2 * a.cols;
   if constexpr (TEAMS > 1) {
-    __shared__ float acc[2][NCH * 512];
-    for (int t = 0; t < TEAMS; ++t) {
-      if (wave == t)
+    constexpr int ROW = 65, PER = NCH * TEAM * 8 * ROW;
+    __shared__ float acc[TEAMS * PER];
+    auto join = [&](const float (&v)[NCH][8], float* out) __attribute__((always_inline)) {
 #pragma unroll
-        for (int k = 0; k < NCH; ++k)
+      for (int k = 0; k < NCH; ++k)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int c = col[k] + i;
-            acc[0][c] = t ? acc[0][c] + dw[k][i] : dw[k][i];
-            acc[1][c] = t ? acc[1][c] + db[k][i] : db[k][i];
-          }
+        for (int i = 0; i < 8; ++i)
+          acc[team * PER + ((k * TEAM + tw) * 8 + i) * ROW + lane] = v[k][i];
       __syncthreads();
-    }
-    for (int c = threadIdx.x; c < a.cols; c += 64 * WAVES) {
-      part[c] = acc[0][c];
-      part[a.cols + c] = acc[1][c];
-    }
+      for (int c = threadIdx.x; c < a.cols; c += 64 * WAVES) {
+        const int at = ((c >> 9) * 8 + (c & 7)) * ROW + ((c >> 3) & 63);
+        float s = acc[at];
+#pragma unroll
+        for (int t = 1; t < TEAMS; ++t) s += acc[t * PER + at];
+        out[c] = s;
+      }
+      __syncthreads();
+    };
+    join(dw, part);
+    join(db, part + a.cols);
   } else {
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
@@ -235,7 +286,7 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* part, in
 
 namespace {
 // Team and chunks for a row of `cols` columns: one wave up to 2048, four up to
-// 8192, sixteen up to 16384; the fewest chunks that hold the row.
+// 8192, eight up to 16384; the fewest chunks that hold the row.
 template <typename F>
 void with_shape(int cols, F&& f) {
   auto go = [&](auto team, auto nch) { f(team, nch); };
@@ -247,24 +298,35 @@ void with_shape(int cols, F&& f) {
   else if (cols <= 4096) MUON_SHAPE(4, 2);
   else if (cols <= 6144) MUON_SHAPE(4, 3);
   else if (cols <= 8192) MUON_SHAPE(4, 4);
-  else MUON_SHAPE(16, 2);
+  else if (cols <= 12288) MUON_SHAPE(8, 3);
+  else MUON_SHAPE(8, 4);
 #undef MUON_SHAPE
 }
-int rows_per_group(int cols) { return cols <= 2048 ? 4 : 1; }
-int groups_for(int rows, int cols, int most) {
-  const int per = rows_per_group(cols);
-  const long long g = ((long long)rows + per - 1) / per;
+// Workgroups for `rows` rows, `teams` to a workgroup, at most `most`.
+int groups_for(int rows, int teams, int most) {
+  const long long g = ((long long)rows + teams - 1) / teams;
   return (int)(g < most ? g : most);
 }
 }  // namespace
 
+#ifndef BACK_GROUPS
+#define BACK_GROUPS 256
+#endif
 // Workgroups of the backward pass, each with one partial sum.
-int norm_backward_groups(int rows, int cols) { return groups_for(rows, cols, 512); }
+int norm_backward_groups(int rows, int cols) {
+  int g = 0;
+  with_shape(cols, [&](auto team, auto) {
+    constexpr int T = decltype(team)::value;
+    g = groups_for(rows, back_waves(T) / T, BACK_GROUPS);
+  });
+  return g;
+}
 
 hipError_t launch_layer_norm(int x_bf16, int out, const NormArgs& a, hipStream_t s) {
   with_shape(a.cols, [&](auto team, auto nch) {
     constexpr int T = decltype(team)::value, N = decltype(nch)::value;
-    const dim3 grid(groups_for(a.rows, a.cols, T > 4 ? 512 : 2048)), block(T > 4 ? 64 * T : 256);
+    const dim3 grid(groups_for(a.rows, T > 4 ? 1 : 4 / T, T > 4 ? 512 : 2048)),
+        block(T > 4 ? 64 * T : 256);
     if (x_bf16) {
       if (out == MUON_BF16)
         hipLaunchKernelGGL((layer_norm_kernel<MUON_BF16, MUON_BF16, T, N>), grid, block, 0, s, a);
@@ -287,7 +349,7 @@ hipError_t launch_layer_norm(int x_bf16, int out, const NormArgs& a, hipStream_t
 hipError_t launch_layer_norm_backward(int dy_bf16, int x, const NormBackArgs& a, hipStream_t s) {
   if (a.groups > 0) with_shape(a.cols, [&](auto team, auto nch) {
     constexpr int T = decltype(team)::value, N = decltype(nch)::value;
-    const dim3 grid(a.groups), block(T > 4 ? 64 * T : 256);
+    const dim3 grid(a.groups), block(64 * back_waves(T));
     auto go = [&](auto dt) {
       constexpr int D = decltype(dt)::value;
       if (x == MUON_BF16)

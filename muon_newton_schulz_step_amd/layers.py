@@ -19,7 +19,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _lib
-from . import (MUON_BF16, MUON_FP32, MUON_OK, MuonError, _check_device, _dtype_code, _stream,
+from . import (MUON_BF16, MUON_FP32, MUON_OK, MuonError, Workspace, _default_ws, _dtype_code,
                _torch, _workspace, lib)
 
 
@@ -55,20 +55,26 @@ class Tensor8:
         if data.dim() != 2 or data.shape[1] != _ld8(cols) or not data.is_contiguous():
             raise ValueError("data must be contiguous, (rows, cols rounded up to 128)")
         rows = data.shape[0]
-        if (scale.dim() != 2 or scale.shape[1] != _scale_ld8(cols) or not scale.is_contiguous()
-                or scale.shape[0] != -(-rows // block_rows)):
+        if scale.shape != (-(-rows // block_rows), _scale_ld8(cols)) or not scale.is_contiguous():
             raise ValueError("scale must be contiguous, (blocks of rows, 4 ceil(cols / 512))")
-        if data.device != scale.device:
+        if data.get_device() != scale.get_device():
             raise ValueError("data and scale must be on one device")
+        self._set(data, scale, rows, cols, block_rows)
+
+    def _set(self, data, scale, rows, cols, block_rows):
         self.data, self.scale, self.cols, self.block_rows = data, scale, cols, block_rows
         self._c = _lib.MuonTensor8(data.data_ptr(), scale.data_ptr(), rows, cols, block_rows)
 
     @classmethod
     def empty(cls, rows: int, cols: int, block_rows: int = 1, device=None):
         torch = _torch()
-        return cls(torch.empty((rows, _ld8(cols)), dtype=torch.float8_e4m3fn, device=device),
-                   torch.empty((-(-rows // block_rows), _scale_ld8(cols)), dtype=torch.uint8,
-                               device=device), cols, block_rows)
+        if block_rows not in (1, 128) or rows < 0 or not 1 <= cols <= _lib.MUON_MAX_COLS8:
+            raise ValueError("rows >= 0, cols in [1, MUON_MAX_COLS8], block_rows 1 or 128")
+        t = cls.__new__(cls)
+        t._set(torch.empty((rows, _ld8(cols)), dtype=torch.float8_e4m3fn, device=device),
+               torch.empty((-(-rows // block_rows), _scale_ld8(cols)), dtype=torch.uint8,
+                           device=device), rows, cols, block_rows)
+        return t
 
     @property
     def rows(self) -> int:
@@ -89,8 +95,10 @@ class Tensor8:
         return f"Tensor8({self.rows} x {self.cols}, blocks of {self.block_rows} x 128)"
 
 
+# The checks below run on every call, where a small one takes a few
+# microseconds on the GPU: they ask each tensor as little as they can.
 def _matrix(t, name: str):
-    """(pointer, row stride) of a 2-D GPU tensor whose rows are dense."""
+    """(pointer, rows, cols, row stride) of a 2-D tensor whose rows are dense."""
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
     rows, cols = t.shape
@@ -99,23 +107,57 @@ def _matrix(t, name: str):
     ld, inner = t.stride()
     if (inner != 1 and cols > 1) or (ld < cols and rows > 1):
         raise ValueError(f"{name}: elements of a row must be adjacent, and rows not overlap")
-    return t.data_ptr(), ld if rows > 1 else cols
+    return t.data_ptr(), rows, cols, ld if rows > 1 else cols
 
 
 def _vector(t, n: int, name: str):
-    if t.dtype != _torch().float32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+    if t.dtype != _torch().float32 or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous fp32 vector of {n} elements")
     return t.data_ptr()
 
 
-def _call(device, name, *args):
+def _device(first, *others) -> int:
+    """The index of the GPU that every tensor (None: no tensor) is on."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError("tensors must be GPU tensors")
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"every tensor must be on cuda:{index}, found {t.device}")
+    return index
+
+
+def _raw_stream(index: int) -> int:
+    torch = _torch()
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get else torch.cuda.current_stream(index).cuda_stream
+
+
+def _scratch(nbytes: int, index: int, workspace):
+    """(pointer, bytes) of the workspace.  The default one of a stream is used
+    there only, so that nothing has to be recorded when it is large enough."""
+    if nbytes == 0:
+        return 0, 0
+    if workspace is None:
+        kept = _default_ws.get((f"cuda:{index}", _raw_stream(index)))
+        if kept is not None and kept.buf is not None and kept.buf.numel() >= nbytes:
+            return kept.buf.data_ptr(), kept.buf.numel()
+    return _workspace(nbytes, _torch().device("cuda", index), workspace)
+
+
+def _tensor_of(workspace):
+    """A workspace given as a tensor, for the device check."""
+    return None if workspace is None or isinstance(workspace, Workspace) else workspace
+
+
+def _call(index: int, name: str, *args):
     torch = _torch()
     fn = getattr(lib(), name)
-    if torch.cuda.current_device() == device.index:
-        st = fn(*args, _stream(device))
+    if torch.cuda.current_device() == index:
+        st = fn(*args, _raw_stream(index))
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, _stream(device))
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
     if st != MUON_OK:
         raise MuonError(st, name)
 
@@ -124,20 +166,19 @@ def quantize8(x, block_rows: int = 1, *, transposed: bool = False, out=None):
     """``x`` (rows, cols), bf16 or fp32, as a Tensor8.  With ``transposed``
     (128-row blocks only) returns (Tensor8 of x, Tensor8 of x^T): the same
     values and scales in both layouts, in one pass."""
-    xp, ldx = _matrix(x, "x")
-    rows, cols = x.shape
+    xp, rows, cols, ldx = _matrix(x, "x")
     code = _dtype_code(x.dtype)
-    if out is None:
-        out = Tensor8.empty(rows, cols, block_rows, x.device)
-    elif out.shape != (rows, cols) or out.block_rows != block_rows:
-        raise ValueError("out must be a Tensor8 of x's shape and block_rows")
-    _check_device(x.device, out=[out.data])
     if transposed and block_rows != 128:
         raise ValueError("a transposed copy needs block_rows=128")
     if transposed and rows == 0:
         raise ValueError("a tensor without rows has no transposed copy")
+    if out is not None and (out.shape != (rows, cols) or out.block_rows != block_rows):
+        raise ValueError("out must be a Tensor8 of x's shape and block_rows")
+    index = _device(x, out.data if out is not None else None)
+    if out is None:
+        out = Tensor8.empty(rows, cols, block_rows, x.device)
     other = Tensor8.empty(cols, rows, 128, x.device) if transposed else None
-    _call(x.device, "muon_quantize8", xp, code, rows, cols, ldx, out._c,
+    _call(index, "muon_quantize8", xp, code, rows, cols, ldx, out._c,
           other._c if transposed else None)
     return (out, other) if transposed else out
 
@@ -147,9 +188,9 @@ def dequantize8(t, dtype=None):
     torch = _torch()
     dtype = dtype or torch.bfloat16
     code = _dtype_code(dtype)
-    _check_device(t.device)
+    index = _device(t.data)
     y = torch.empty((t.rows, t.cols), dtype=dtype, device=t.device)
-    _call(t.device, "muon_dequantize8", t._c, y.data_ptr(), code, t.cols)
+    _call(index, "muon_dequantize8", t._c, y.data_ptr(), code, t.cols)
     return y
 
 
@@ -159,15 +200,16 @@ def matmul8(a, b, *, out_dtype=None, out=None):
     torch = _torch()
     if a.cols != b.cols:
         raise ValueError(f"a and b must have the same number of columns: {a.cols}, {b.cols}")
+    index = _device(a.data, b.data, out)
+    m, n = a.data.shape[0], b.data.shape[0]
     if out is None:
-        out = torch.empty((a.rows, b.rows), dtype=out_dtype or torch.bfloat16, device=a.device)
-        yp, ldy = out.data_ptr(), max(b.rows, 1)
+        out = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=a.data.device)
+        yp, ldy = out.data_ptr(), max(n, 1)
     else:
-        if tuple(out.shape) != (a.rows, b.rows) or (out_dtype or out.dtype) != out.dtype:
+        if out.shape != (m, n) or (out_dtype or out.dtype) != out.dtype:
             raise ValueError("out must be (a.rows, b.rows) and of out_dtype")
-        yp, ldy = _matrix(out, "out") if b.rows else (0, 1)
-    _check_device(a.device, b=[b.data], out=[out])
-    _call(a.device, "muon_matmul8", a._c, b._c, yp, _dtype_code(out.dtype), ldy)
+        yp, _, _, ldy = _matrix(out, "out") if n else (0, m, n, 1)
+    _call(index, "muon_matmul8", a._c, b._c, yp, _dtype_code(out.dtype), ldy)
     return out
 
 
@@ -180,28 +222,22 @@ def weight_grad(dy, x, *, out_dtype=None, out=None, accumulate: bool = False, wo
     gradient ``dy`` (tokens, n), bf16, and its input ``x``, a Tensor8 (tokens,
     k).  fp32 (default) or bf16; ``accumulate`` adds to an fp32 ``out``."""
     torch = _torch()
-    dyp, lddy = _matrix(dy, "dy")
-    tokens, n = dy.shape
+    dyp, tokens, n, lddy = _matrix(dy, "dy")
+    k = x.cols
     if x.rows != tokens:
         raise ValueError(f"dy and x must have the same number of rows: {tokens}, {x.rows}")
-    if out is None:
-        if accumulate:
-            raise ValueError("accumulate needs out")
-        out = torch.empty((n, x.cols), dtype=out_dtype or torch.float32, device=dy.device)
-    elif (tuple(out.shape) != (n, x.cols) or (out_dtype or out.dtype) != out.dtype
-          or not out.is_contiguous()):
+    if out is None and accumulate:
+        raise ValueError("accumulate needs out")
+    if out is not None and (out.shape != (n, k) or (out_dtype or out.dtype) != out.dtype
+                            or not out.is_contiguous()):
         raise ValueError("out must be contiguous, (dy columns, x columns), and of out_dtype")
-    _check_device(dy.device, x=[x.data], out=[out], workspace=[_raw(workspace)])
-    need = weight_grad_workspace_bytes(tokens, n, x.cols)
-    wptr, wbytes = _workspace(need, dy.device, workspace) if need else (0, 0)
-    _call(dy.device, "muon_weight_grad", dyp, _dtype_code(dy.dtype), lddy, tokens, n, x._c,
+    index = _device(dy, x.data, out, _tensor_of(workspace))
+    if out is None:
+        out = torch.empty((n, k), dtype=out_dtype or torch.float32, device=dy.device)
+    wptr, wbytes = _scratch(lib().muon_weight_grad_workspace_bytes(tokens, n, k), index, workspace)
+    _call(index, "muon_weight_grad", dyp, _dtype_code(dy.dtype), lddy, tokens, n, x._c,
           out.data_ptr(), _dtype_code(out.dtype), 1 if accumulate else 0, wptr, wbytes)
     return out
-
-
-def _raw(workspace):
-    """A workspace given as a tensor, for the device check."""
-    return workspace if hasattr(workspace, "data_ptr") else None
 
 
 def layer_norm(x, weight, bias=None, *, eps: float = 1e-5, out_dtype=None):
@@ -209,14 +245,12 @@ def layer_norm(x, weight, bias=None, *, eps: float = 1e-5, out_dtype=None):
     ``out_dtype`` bf16 or fp32 (default: x's), or torch.float8_e4m3fn for a
     Tensor8 with blocks of 1 x 128.  ``weight`` and ``bias`` are fp32."""
     torch = _torch()
-    xp, ldx = _matrix(x, "x")
-    rows, cols = x.shape
-    device = x.device
+    xp, rows, cols, ldx = _matrix(x, "x")
     wp = _vector(weight, cols, "weight")
     bp = _vector(bias, cols, "bias") if bias is not None else None
-    _check_device(device, weight=[weight], bias=[bias])
-    stats = torch.empty((2, rows), dtype=torch.float32, device=device)
-    mean, rstd = stats[0], stats[1]
+    index = _device(x, weight, bias)
+    device = x.device
+    mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=device).unbind(0)
     out_dtype = out_dtype or x.dtype
     if out_dtype == torch.float8_e4m3fn:
         y = Tensor8.empty(rows, cols, 1, device)
@@ -225,9 +259,8 @@ def layer_norm(x, weight, bias=None, *, eps: float = 1e-5, out_dtype=None):
         code = _dtype_code(out_dtype)
         y = torch.empty((rows, cols), dtype=out_dtype, device=device)
         yp, ldy, y8 = y.data_ptr(), cols, None
-    sp = stats.data_ptr()
-    _call(device, "muon_layer_norm", xp, _dtype_code(x.dtype), ldx, rows, cols, wp, bp, eps,
-          yp, code, ldy, y8, sp, sp + 4 * rows)
+    _call(index, "muon_layer_norm", xp, _dtype_code(x.dtype), ldx, rows, cols, wp, bp, eps,
+          yp, code, ldy, y8, mean.data_ptr(), rstd.data_ptr())
     return y, mean, rstd
 
 
@@ -242,34 +275,36 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, bias: bool = True, dweight
     ``dbias`` (fp32) may be given, and are added to with ``accumulate``;
     ``bias`` False: no dbias (None)."""
     torch = _torch()
-    dyp, lddy = _matrix(dy, "dy")
-    rows, cols = dy.shape
-    device = dy.device
-    if tuple(x.shape) != (rows, cols):
-        raise ValueError("x and dy must have the same shape")
+    dyp, rows, cols, lddy = _matrix(dy, "dy")
     if isinstance(x, Tensor8):
+        same = x.shape == (rows, cols)
         xp, xcode, ldx, x8, xt = None, MUON_BF16, cols, x._c, x.data
     else:
-        xp, ldx = _matrix(x, "x")
+        same = x.shape == dy.shape
+        xp, _, _, ldx = _matrix(x, "x")
         xcode, x8, xt = _dtype_code(x.dtype), None, x
+    if not same:
+        raise ValueError("x and dy must have the same shape")
     if not bias and dbias is not None:
         raise ValueError("dbias was given with bias=False")
     if accumulate and (dweight is None or (bias and dbias is None)):
         raise ValueError("accumulate needs dweight and dbias")
-    wp, mp, rp = (_vector(t, n, name) for t, n, name in (
-        (weight, cols, "weight"), (mean, rows, "mean"), (rstd, rows, "rstd")))
+    wp = _vector(weight, cols, "weight")
+    mp, rp = _vector(mean, rows, "mean"), _vector(rstd, rows, "rstd")
+    dwp = _vector(dweight, cols, "dweight") if dweight is not None else 0
+    dbp = _vector(dbias, cols, "dbias") if dbias is not None else None
+    index = _device(dy, xt, weight, mean, rstd, dweight, dbias, _tensor_of(workspace))
+    device = dy.device
     dx = torch.empty((rows, cols), dtype=dy.dtype, device=device)
     if dweight is None:
         dweight = torch.empty(cols, dtype=torch.float32, device=device)
+        dwp = dweight.data_ptr()
     if bias and dbias is None:
         dbias = torch.empty(cols, dtype=torch.float32, device=device)
-    dwp = _vector(dweight, cols, "dweight")
-    dbp = _vector(dbias, cols, "dbias") if bias else None
-    _check_device(device, x=[xt], weight=[weight], mean=[mean], rstd=[rstd], dweight=[dweight],
-                  dbias=[dbias], workspace=[_raw(workspace)])
-    need = layer_norm_backward_workspace_bytes(rows, cols)
-    wptr, wbytes = _workspace(need, device, workspace) if need else (0, 0)
-    _call(device, "muon_layer_norm_backward", dyp, _dtype_code(dy.dtype), lddy, xp, xcode, ldx,
+        dbp = dbias.data_ptr()
+    wptr, wbytes = _scratch(lib().muon_layer_norm_backward_workspace_bytes(rows, cols), index,
+                            workspace)
+    _call(index, "muon_layer_norm_backward", dyp, _dtype_code(dy.dtype), lddy, xp, xcode, ldx,
           x8, rows, cols, wp, mp, rp, dx.data_ptr(), cols, dwp, dbp, 1 if accumulate else 0,
           wptr, wbytes)
     return dx, dweight, dbias

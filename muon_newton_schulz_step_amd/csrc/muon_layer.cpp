@@ -68,7 +68,7 @@ bool pieces_fit(int rows, int cols) {
   return (double)rows * (double)((cols + 511) / 512) < 4294967296.0;
 }
 bool tiles_fit(long long rows, long long cols) {
-  return (double)((rows + 127) / 128) * (double)((cols + 127) / 128) < 2147483648.0;
+  return (double)((rows + 63) / 64) * (double)((cols + 63) / 64) < 2147483648.0;
 }
 int status_of(hipError_t e) { return e == hipSuccess ? MUON_OK : MUON_ERR_HIP; }
 

@@ -17,8 +17,7 @@
 //
 // Two kernels:
 //   tiles   both operands through LDS, for many rows of a: bound by the MFMAs;
-//   rows    few rows of a (up to kFewRows): bound by reading b once, so always
-//           exact.
+//   rows    few rows of a (up to 32): bound by reading b once, so always exact.
 #include "muon_gemm.h"
 
 #include "fp8_device.h"
@@ -274,31 +273,35 @@ __global__ __launch_bounds__(64 * WGM * WGN) void matmul8_tile_kernel(Matmul8Arg
 }
 
 // ---------------------------------------------------------------- rows
-// Up to 16 MF rows m.  A workgroup takes 16 columns n and its 8 waves share the
-// blocks of k between them; operands come straight from memory (each row of b
-// is used once) and go to bf16 in registers: four v_mfma_f32_16x16x32_bf16 per
-// block and 16 rows.  The waves' sums are added in their order through LDS.
-constexpr int kFewRows = 64, kFewWaves = 8;
+// Up to 16 MF rows m.  A workgroup takes 16 NF columns n and its 8 waves share
+// the blocks of k between them; operands come straight from memory (each row of
+// b is used once) and go to bf16 in registers: four v_mfma_f32_16x16x32_bf16 per
+// block and 16 x 16 results.  The waves' sums are added in their order through
+// LDS.  NF = 2 reads a half as often, once there are workgroups enough.
+constexpr int kFewWaves = 8;
 
-template <int MF, typename Y>
+template <int MF, int NF, typename Y>
 __global__ __launch_bounds__(64 * kFewWaves) void matmul8_rows_kernel(Matmul8Args g) {
-  __shared__ f32x4_t sums[kFewWaves][MF][64];
+  __shared__ f32x4_t sums[kFewWaves][MF * NF][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int n0 = (int)blockIdx.x * 16;
+  const int n0 = (int)blockIdx.x * 16 * NF;
   const int r = lane & 15, grp = lane >> 4;
   const int nb = g.ld / 128;
-  const int n = n0 + r < g.n ? n0 + r : g.n - 1;
-  const unsigned char* pb = g.b + (long long)n * g.ld + grp * 16;
-  const unsigned char* psb = g.sb + (long long)(n >> g.shift_b) * g.sld;
-  const unsigned char* pa[MF];
-  const unsigned char* psa[MF];
-  f32x4_t acc[MF];
+  const unsigned char *pb[NF], *psb[NF], *pa[MF], *psa[MF];
+  f32x4_t acc[NF][MF];
+#pragma unroll
+  for (int i = 0; i < NF; ++i) {
+    const int n = n0 + 16 * i + r < g.n ? n0 + 16 * i + r : g.n - 1;
+    pb[i] = g.b + (long long)n * g.ld + grp * 16;
+    psb[i] = g.sb + (long long)(n >> g.shift_b) * g.sld;
+  }
 #pragma unroll
   for (int f = 0; f < MF; ++f) {
     const int m = 16 * f + r < g.m ? 16 * f + r : g.m - 1;
     pa[f] = g.a + (long long)m * g.ld + grp * 16;
     psa[f] = g.sa + (long long)(m >> g.shift_a) * g.sld;
-    acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NF; ++i) acc[i][f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   }
   // chunks grp and grp + 4 of the block's eight: each load of a wave takes 64
   // consecutive bytes of 16 rows
@@ -317,27 +320,36 @@ __global__ __launch_bounds__(64 * kFewWaves) void matmul8_rows_kernel(Matmul8Arg
                               bf16_of_e4m3(c[2 * (e & 1)], c[2 * (e & 1) + 1], f.scale));
   };
   for (int kb = wave; kb < nb; kb += kFewWaves) {
-    const Frag fb = load(pb, psb, kb);
-    Frag fa[MF];
+    Frag fb[NF], fa[MF];
+#pragma unroll
+    for (int i = 0; i < NF; ++i) fb[i] = load(pb[i], psb[i], kb);
 #pragma unroll
     for (int f = 0; f < MF; ++f) fa[f] = load(pa[f], psa[f], kb);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const bf16x8_t wb = bf16(fb, e);
+      bf16x8_t wb[NF];
 #pragma unroll
-      for (int f = 0; f < MF; ++f)
-        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb, bf16(fa[f], e), acc[f], 0, 0, 0);
+      for (int i = 0; i < NF; ++i) wb[i] = bf16(fb[i], e);
+#pragma unroll
+      for (int f = 0; f < MF; ++f) {
+        const bf16x8_t wa = bf16(fa[f], e);
+#pragma unroll
+        for (int i = 0; i < NF; ++i)
+          acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb[i], wa, acc[i][f], 0, 0, 0);
+      }
     }
   }
 #pragma unroll
-  for (int f = 0; f < MF; ++f) sums[wave][f][lane] = acc[f];
-  __syncthreads();
-  // acc[f]: row m = 16 f + lane % 16, columns n0 + 4 (lane / 16) + 0 .. 3
-  for (int f = wave; f < MF; f += kFewWaves) {
-    f32x4_t s = sums[0][f][lane];
+  for (int i = 0; i < NF; ++i)
 #pragma unroll
-    for (int w = 1; w < kFewWaves; ++w) s += sums[w][f][lane];
-    const int m = 16 * f + r, c = n0 + 4 * grp;
+    for (int f = 0; f < MF; ++f) sums[wave][i * MF + f][lane] = acc[i][f];
+  __syncthreads();
+  // acc[i][f]: row m = 16 f + lane % 16, columns n0 + 16 i + 4 (lane / 16) + 0 .. 3
+  for (int t = wave; t < MF * NF; t += kFewWaves) {
+    f32x4_t s = sums[0][t][lane];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) s += sums[w][t][lane];
+    const int m = 16 * (t % MF) + r, c = n0 + 16 * (t / MF) + 4 * grp;
     if (m < g.m) {
       Y* y = static_cast<Y*>(g.y) + (long long)m * g.ldy + c;
 #pragma unroll
@@ -368,14 +380,23 @@ void tiles(Matmul8Args a, hipStream_t s) {
 
 template <typename Y>
 void go(const Matmul8Args& a, hipStream_t s) {
-  if (a.m <= kFewRows) {
-    const dim3 grid((a.n + 15) / 16), block(64 * kFewWaves);
-    if (a.m <= 16)
-      hipLaunchKernelGGL((matmul8_rows_kernel<1, Y>), grid, block, 0, s, a);
-    else if (a.m <= 32)
-      hipLaunchKernelGGL((matmul8_rows_kernel<2, Y>), grid, block, 0, s, a);
+  // Few rows.  32 columns to a workgroup where that leaves 256 workgroups and
+  // enough rows share the second half's saving (16 x 8192 x 4096: 11.1 -> 8.7 us,
+  // 32 x 8192 x 4096: 16.6 -> 11.7 us; but 1 x 8192 x 8192: 13 -> 20 us, 16 x 8192
+  // x 8192: 20 -> 22 us).  Past 16 rows a very wide product is faster in tiles (32
+  // x 16384 x 4096: 22.8 -> 17.6 us).
+  if (a.m <= 16 || (a.m <= 32 && a.n < 16384)) {
+    const dim3 block(64 * kFewWaves);
+    const bool two = a.n >= 8192 && (a.m > 16 || (a.m > 8 && a.ld <= 4096));
+    const dim3 grid(two ? (a.n + 31) / 32 : (a.n + 15) / 16);
+    if (a.m <= 16 && !two)
+      hipLaunchKernelGGL((matmul8_rows_kernel<1, 1, Y>), grid, block, 0, s, a);
+    else if (a.m <= 16)
+      hipLaunchKernelGGL((matmul8_rows_kernel<1, 2, Y>), grid, block, 0, s, a);
+    else if (!two)
+      hipLaunchKernelGGL((matmul8_rows_kernel<2, 1, Y>), grid, block, 0, s, a);
     else
-      hipLaunchKernelGGL((matmul8_rows_kernel<4, Y>), grid, block, 0, s, a);
+      hipLaunchKernelGGL((matmul8_rows_kernel<2, 2, Y>), grid, block, 0, s, a);
     return;
   }
   // The tile by the time of the fullest CU, in us per k-tile.  Measured: 256 x

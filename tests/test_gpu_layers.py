@@ -132,7 +132,7 @@ def product_case(m, n, k, ba, bb, out, seed=0):
     ref, mag = av @ bv.T, np.abs(av) @ np.abs(bv).T
     bound = 2 * U * (k + 1) * mag
     if out == BF16:
-        bound = bound + (CUT8 * mag if m > 64 else 0.0)
+        bound = bound + (CUT8 * mag if m > 16 else 0.0)
         bound = bound + HALF[BF16] * (np.abs(ref) + bound)
         # the roundings to bf16 are independent and uniform: 2^-9 relative at most
         # in the root mean square (2^-8 / sqrt(3) of a value just above a power
@@ -148,7 +148,8 @@ def product_case(m, n, k, ba, bb, out, seed=0):
 @pytest.mark.parametrize("m,n,k", [
     (1, 1, 1), (1, 15, 128), (1, 1283, 770), (2, 100, 515), (16, 16, 256), (17, 33, 1283), (32, 257, 130),
     (33, 64, 640), (64, 300, 2050), (65, 1, 128), (65, 129, 300), (100, 259, 129), (128, 128, 128),
-    (129, 511, 896), (300, 1000, 1283), (1000, 77, 513)])
+    (129, 511, 896), (300, 1000, 1283), (1000, 77, 513), (9, 8200, 300), (16, 8192, 4200),
+    (31, 8195, 129), (20, 16400, 260)])
 def test_matmul8(m, n, k, out):
     product_case(m, n, k, 1, 128, out, seed=m)
 

@@ -40,9 +40,14 @@ __device__ __forceinline__ void wait_lgkm0() {
 // arrive.  The waves meet before the last substep, whose operands are in
 // registers by then, and read the next tile's first ones during it.  After each
 // MFMA comes its share of the substep's LDS reads and writes.
-//   8192 tokens, 4096 x 4096, 256 x 256 tiles: 232 us, 1.19 PFLOP/s (393 us
+// Token tiles below the ragged edges are loaded without a branch, in line with
+// the MFMAs.
+//   8192 tokens, 4096 x 4096, 256 x 256 tiles: 220 us, 1.25 PFLOP/s (393 us
 //   with 128 x 128 tiles on 4 waves, everything loaded and stored at the tile's
-//   ends, and no order pinned; a library's plain bf16 product runs at 1.41).
+//   ends, and no order pinned; 234 us with a branch around each load; a
+//   library's plain bf16 product of 8192^3 runs at 1.41).  The MFMAs are busy
+//   half the time, the LDS a third; neither reading operands two substeps ahead
+//   nor loading two token tiles ahead changed that.
 
 template <int BN, int BK, int WGN, int WGK, typename W>
 __global__ __launch_bounds__(64 * WGN * WGK) void weight_grad_kernel(WeightGradArgs g) {
@@ -80,36 +85,43 @@ __global__ __launch_bounds__(64 * WGN * WGK) void weight_grad_kernel(WeightGradA
   // A chunk past dy's or x's last column reads the tile's first one, and one
   // across dy's last column reads into the next row: what comes of them is not
   // stored.  Only the last row has no next one, and rows past it must be zero:
-  // the last token tile is loaded element by element where that matters.
-  auto gload = [&](int kt) __attribute__((always_inline)) {
+  // from token tile `safe` on, loads look at each chunk.
+  const int safe = n_all ? g.tokens / kTileT : (g.tokens - 1) / kTileT;
+  auto gload = [&](int kt, auto plain) __attribute__((always_inline)) {
     const int t0 = kt * kTileT;
-    const bool all = t0 + kTileT <= g.tokens;
     const bf16_t* dyb = static_cast<const bf16_t*>(g.dy) + (long long)t0 * g.lddy + n0;
     const unsigned char* xb = g.x + (long long)t0 * g.ld + k0;
     const unsigned char* sb = g.sx + (long long)(t0 >> g.shift) * g.sld + (k0 >> 7);
-    if (n_all ? all : t0 + kTileT < g.tokens) {
 #pragma unroll
-      for (int i = 0; i < PN; ++i)
-        __builtin_memcpy(&rd[i], dyb + (long long)(NT / UN * i) * g.lddy + dy_off, 16);
-    } else {
-#pragma unroll
-      for (int i = 0; i < PN; ++i) {
+    for (int i = 0; i < PN; ++i) {
+      const bf16_t* p = dyb + (long long)(NT / UN * i) * g.lddy + dy_off;
+      if constexpr (decltype(plain)::value) {
+        __builtin_memcpy(&rd[i], p, 16);
+      } else {
         float v[8];
-        load8_edge(dyb + (long long)(NT / UN * i) * g.lddy + dy_off,
-                   t0 + tn + NT / UN * i < g.tokens ? g.n - n : 0, v);
+        load8_edge(p, t0 + tn + NT / UN * i < g.tokens ? g.n - n : 0, v);
 #pragma unroll
         for (int e = 0; e < 4; ++e) rd[i][e] = pack_bf16(v[2 * e], v[2 * e + 1]);
       }
     }
 #pragma unroll
     for (int i = 0; i < PK; ++i) {
-      rx[i] = u32x2_t{0u, 0u};
-      sx[i] = 127;
-      if (all || t0 + tk + NT / UK * i < g.tokens) {
-        rx[i] = *reinterpret_cast<const u32x2_t*>(xb + (long long)(NT / UK * i) * g.ld + x_off);
-        sx[i] = sb[(g.shift ? 0 : (long long)(NT / UK * i) * g.sld) + s_off];
+      const unsigned char* p = xb + (long long)(NT / UK * i) * g.ld + x_off;
+      const unsigned char* s = sb + (g.shift ? 0 : (long long)(NT / UK * i) * g.sld) + s_off;
+      if (decltype(plain)::value || t0 + tk + NT / UK * i < g.tokens) {
+        rx[i] = *reinterpret_cast<const u32x2_t*>(p);
+        sx[i] = *s;
+      } else {
+        rx[i] = u32x2_t{0u, 0u};
+        sx[i] = 127;
       }
     }
+  };
+  auto gload_any = [&](int kt) __attribute__((always_inline)) {
+    if (kt < safe)
+      gload(kt, std::true_type{});
+    else
+      gload(kt, std::false_type{});
   };
   auto lstore = [&](int st) __attribute__((always_inline)) {
 #pragma unroll
@@ -183,15 +195,24 @@ __global__ __launch_bounds__(64 * WGN * WGK) void weight_grad_kernel(WeightGradA
     });
   };
   using Z = std::integral_constant<int, 0>;
-  auto ttile = [&](int kt, int cur, int nxt) __attribute__((always_inline)) {
+  // token tile kt from stage cur; the registers hold tile kt + 1, which goes to
+  // stage nxt, and then take tile kt + 2 (`plain`: it is there and below safe)
+  auto ttile = [&](int kt, int cur, int nxt, auto plain) __attribute__((always_inline)) {
     lstore(nxt);
     fload(cur, 1, 1);
     mfmas(0);
     pins(std::integral_constant<int, PN + PK>{}, Z{});
-    if (kt + 2 < t_end) gload(kt + 2);
-    fload(cur, 2, 0);
-    mfmas(1);
-    pins(Z{}, Z{});
+    if constexpr (decltype(plain)::value) {
+      gload(kt + 2, plain);
+      fload(cur, 2, 0);
+      mfmas(1);
+      pins(Z{}, std::integral_constant<int, PN + 2 * PK>{});
+    } else {
+      if (kt + 2 < t_end) gload_any(kt + 2);
+      fload(cur, 2, 0);
+      mfmas(1);
+      pins(Z{}, Z{});
+    }
     fload(cur, 3, 1);
     mfmas(0);
     pins(Z{}, Z{});
@@ -204,15 +225,20 @@ __global__ __launch_bounds__(64 * WGN * WGK) void weight_grad_kernel(WeightGradA
     pins(Z{}, Z{});
   };
   if (t_first < t_end) {
-    gload(t_first);
+    gload_any(t_first);
     lstore(0);
-    if (t_first + 1 < t_end) gload(t_first + 1);
+    if (t_first + 1 < t_end) gload_any(t_first + 1);
     wait_lgkm0();
     barrier_no_fence();
     fload(0, 0, 0);
-    for (int kt = t_first; kt < t_end; kt += 2) {
-      ttile(kt, 0, 1);
-      if (kt + 1 < t_end) ttile(kt + 1, 1, 0);
+    int kt = t_first;
+    for (; kt + 3 < t_end && kt + 3 < safe; kt += 2) {
+      ttile(kt, 0, 1, std::true_type{});
+      ttile(kt + 1, 1, 0, std::true_type{});
+    }
+    for (; kt < t_end; kt += 2) {
+      ttile(kt, 0, 1, std::false_type{});
+      if (kt + 1 < t_end) ttile(kt + 1, 1, 0, std::false_type{});
     }
   }
 
@@ -269,19 +295,20 @@ __global__ __launch_bounds__(256) void weight_grad_join_kernel(const float* part
 
 // The tile and the number of token splits.  A CU holds one workgroup of 256 x
 // 256 or 256 x 128 tiles, or two of 128 x 128 ones, all of 8 waves.  Measured per
-// token tile: 1.78 us (256 x 256), 1.15 us (256 x 128), and for 128 x 128
-// 0.78 us alone on its CU, 1.3 us for two.  The result and its parts move at
+// token tile: 1.7 us (256 x 256), 0.95 us (256 x 128), and for 128 x 128
+// 0.55 us alone on its CU, 1.23 us for two.  The result and its parts move at
 // about 4.7 TB/s, written and read, and a second launch costs about 3 us.  The
-// plan takes the smallest sum.  (4096 tokens, 1280 x 5120: 104 us, 72 us,
-// 78 us with the three tiles; 16384 tokens, 768 x 1024, in 10 parts: 56, 41,
-// 44 us; 8192 tokens, 4096 x 4096: 232, 288, 333 us.)
+// plan takes the smallest sum.  (4096 tokens, 1280 x 5120: 62 us with 256 x
+// 128, 104 and 78 us with the others, these two before their loads went in line;
+// 16384 tokens, 768 x 1024: 38.5 us in 10 parts of 256 x 128, 40.5 us in 5 of
+// 128 x 128; 8192 tokens, 4096 x 4096: 220, 257, 314 us.)
 WeightGradPlan weight_grad_plan(int tokens, int n, int k) {
   struct Kind {
     int bn, bk, per_cu;
     double one, full;  // us per token tile: alone on its CU, all places taken
   };
   static const Kind kinds[3] = {
-      {256, 256, 1, 1.78, 1.78}, {256, 128, 1, 1.15, 1.15}, {128, 128, 2, 0.78, 1.3}};
+      {256, 256, 1, 1.7, 1.7}, {256, 128, 1, 0.95, 0.95}, {128, 128, 2, 0.55, 1.23}};
   const int tt = (int)(((long long)tokens + kTileT - 1) / kTileT);
   WeightGradPlan best{};
   double least = 0.0;

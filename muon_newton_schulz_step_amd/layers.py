@@ -71,8 +71,8 @@ class Tensor8:
         if block_rows not in (1, 128) or rows < 0 or not 1 <= cols <= _lib.MUON_MAX_COLS8:
             raise ValueError("rows >= 0, cols in [1, MUON_MAX_COLS8], block_rows 1 or 128")
         t = cls.__new__(cls)
-        t._set(torch.empty((rows, _ld8(cols)), dtype=torch.float8_e4m3fn, device=device),
-               torch.empty((-(-rows // block_rows), _scale_ld8(cols)), dtype=torch.uint8,
+        t._set(torch.empty(rows, _ld8(cols), dtype=torch.float8_e4m3fn, device=device),
+               torch.empty(-(-rows // block_rows), _scale_ld8(cols), dtype=torch.uint8,
                            device=device), rows, cols, block_rows)
         return t
 
@@ -189,7 +189,7 @@ def dequantize8(t, dtype=None):
     dtype = dtype or torch.bfloat16
     code = _dtype_code(dtype)
     index = _device(t.data)
-    y = torch.empty((t.rows, t.cols), dtype=dtype, device=t.device)
+    y = torch.empty(t.rows, t.cols, dtype=dtype, device=t.device)
     _call(index, "muon_dequantize8", t._c, y.data_ptr(), code, t.cols)
     return y
 
@@ -203,7 +203,7 @@ def matmul8(a, b, *, out_dtype=None, out=None):
     index = _device(a.data, b.data, out)
     m, n = a.data.shape[0], b.data.shape[0]
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype or torch.bfloat16, device=a.data.device)
+        out = torch.empty(m, n, dtype=out_dtype or torch.bfloat16, device=a.data.device)
         yp, ldy = out.data_ptr(), max(n, 1)
     else:
         if out.shape != (m, n) or (out_dtype or out.dtype) != out.dtype:
@@ -233,7 +233,7 @@ def weight_grad(dy, x, *, out_dtype=None, out=None, accumulate: bool = False, wo
         raise ValueError("out must be contiguous, (dy columns, x columns), and of out_dtype")
     index = _device(dy, x.data, out, _tensor_of(workspace))
     if out is None:
-        out = torch.empty((n, k), dtype=out_dtype or torch.float32, device=dy.device)
+        out = torch.empty(n, k, dtype=out_dtype or torch.float32, device=dy.device)
     wptr, wbytes = _scratch(lib().muon_weight_grad_workspace_bytes(tokens, n, k), index, workspace)
     _call(index, "muon_weight_grad", dyp, _dtype_code(dy.dtype), lddy, tokens, n, x._c,
           out.data_ptr(), _dtype_code(out.dtype), 1 if accumulate else 0, wptr, wbytes)
@@ -250,14 +250,14 @@ def layer_norm(x, weight, bias=None, *, eps: float = 1e-5, out_dtype=None):
     bp = _vector(bias, cols, "bias") if bias is not None else None
     index = _device(x, weight, bias)
     device = x.device
-    mean, rstd = torch.empty((2, rows), dtype=torch.float32, device=device).unbind(0)
+    mean, rstd = weight.new_empty(rows), weight.new_empty(rows)
     out_dtype = out_dtype or x.dtype
     if out_dtype == torch.float8_e4m3fn:
         y = Tensor8.empty(rows, cols, 1, device)
         yp, code, ldy, y8 = None, MUON_BF16, cols, y._c
     else:
         code = _dtype_code(out_dtype)
-        y = torch.empty((rows, cols), dtype=out_dtype, device=device)
+        y = torch.empty(rows, cols, dtype=out_dtype, device=device)
         yp, ldy, y8 = y.data_ptr(), cols, None
     _call(index, "muon_layer_norm", xp, _dtype_code(x.dtype), ldx, rows, cols, wp, bp, eps,
           yp, code, ldy, y8, mean.data_ptr(), rstd.data_ptr())
@@ -295,12 +295,12 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, bias: bool = True, dweight
     dbp = _vector(dbias, cols, "dbias") if dbias is not None else None
     index = _device(dy, xt, weight, mean, rstd, dweight, dbias, _tensor_of(workspace))
     device = dy.device
-    dx = torch.empty((rows, cols), dtype=dy.dtype, device=device)
+    dx = torch.empty(rows, cols, dtype=dy.dtype, device=device)
     if dweight is None:
-        dweight = torch.empty(cols, dtype=torch.float32, device=device)
+        dweight = weight.new_empty(cols)
         dwp = dweight.data_ptr()
     if bias and dbias is None:
-        dbias = torch.empty(cols, dtype=torch.float32, device=device)
+        dbias = weight.new_empty(cols)
         dbp = dbias.data_ptr()
     wptr, wbytes = _scratch(lib().muon_layer_norm_backward_workspace_bytes(rows, cols), index,
                             workspace)

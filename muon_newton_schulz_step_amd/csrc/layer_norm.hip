@@ -261,25 +261,26 @@ __global__ __launch_bounds__(64 * back_waves(TEAM)) void layer_norm_back_kernel(
   }
 }
 
-// dw and db from the workgroups' partial sums, in their order: 64 columns
-// per workgroup, 16 waves over the partial rows, joined in LDS.
+// dw and db from the workgroups' partial sums, in their order: 32 columns per
+// workgroup, 32 threads to a column, so that each thread's loads (8 of 256
+// partial rows) are all on their way at once; joined in LDS.
 __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* part, int groups, int cols,
                                                            float* dw, float* db, int accumulate) {
-  __shared__ float acc[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
+  __shared__ float acc[32][33];
+  const int x = threadIdx.x & 31, g0 = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + x;
   float* out = blockIdx.y ? db : dw;
   const float* p = part + (blockIdx.y ? cols : 0) + c;
   float s = 0.f;
   if (c < cols)
 #pragma unroll 8
-    for (int g = wave; g < groups; g += 16) s += p[(long long)g * 2 * cols];
-  acc[wave][lane] = s;
+    for (int g = g0; g < groups; g += 32) s += p[(long long)g * 2 * cols];
+  acc[g0][x] = s;
   __syncthreads();
-  if (wave == 0 && c < cols) {
+  if (g0 == 0 && c < cols) {
     s = 0.f;
 #pragma unroll
-    for (int w = 0; w < 16; ++w) s += acc[w][lane];
+    for (int g = 0; g < 32; ++g) s += acc[g][x];
     out[c] = accumulate ? out[c] + s : s;
   }
 }
@@ -309,15 +310,13 @@ int groups_for(int rows, int teams, int most) {
 }
 }  // namespace
 
-#ifndef BACK_GROUPS
-#define BACK_GROUPS 256
-#endif
-// Workgroups of the backward pass, each with one partial sum.
+// Workgroups of the backward pass, each with one partial sum: one per CU, which
+// holds a CU's share of the registers and keeps the partial sums few.
 int norm_backward_groups(int rows, int cols) {
   int g = 0;
   with_shape(cols, [&](auto team, auto) {
     constexpr int T = decltype(team)::value;
-    g = groups_for(rows, back_waves(T) / T, BACK_GROUPS);
+    g = groups_for(rows, back_waves(T) / T, 256);
   });
   return g;
 }
@@ -366,7 +365,7 @@ hipError_t launch_layer_norm_backward(int dy_bf16, int x, const NormBackArgs& a,
   });
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  hipLaunchKernelGGL(norm_reduce_kernel, dim3((a.cols + 63) / 64, a.dbias ? 2 : 1), dim3(1024), 0,
+  hipLaunchKernelGGL(norm_reduce_kernel, dim3((a.cols + 31) / 32, a.dbias ? 2 : 1), dim3(1024), 0,
                      s, a.part, a.groups, a.cols, a.dweight, a.dbias, a.accumulate);
   return hipGetLastError();
 }

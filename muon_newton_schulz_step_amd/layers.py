@@ -19,8 +19,31 @@ from __future__ import annotations
 import ctypes
 
 from . import _lib
-from . import (MUON_BF16, MUON_FP32, MUON_OK, MuonError, Workspace, _default_ws, _dtype_code,
-               _torch, _workspace, lib)
+from . import (MUON_BF16, MUON_FP32, MUON_OK, MuonError, Workspace, _default_ws, _workspace,
+               lib)
+
+# torch, its raw stream query and the element types' codes, from the first call on
+_T = None
+_stream_of = None
+_codes: dict = {}
+
+
+def _torch():
+    global _T, _stream_of
+    if _T is None:
+        import torch
+        _codes.update({torch.bfloat16: MUON_BF16, torch.float32: MUON_FP32})
+        _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _T = torch
+    return _T
+
+
+def _dtype_code(dtype) -> int:
+    code = _codes.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} (bfloat16 or float32)")
+    return code
 
 
 def _ld8(cols: int) -> int:
@@ -45,7 +68,7 @@ class Tensor8:
     __slots__ = ("data", "scale", "cols", "block_rows", "_c")
 
     def __init__(self, data, scale, cols: int, block_rows: int = 1):
-        torch = _torch()
+        torch = _T or _torch()
         if block_rows not in (1, 128):
             raise ValueError("block_rows must be 1 or 128")
         if not 1 <= cols <= _lib.MUON_MAX_COLS8:
@@ -67,7 +90,7 @@ class Tensor8:
 
     @classmethod
     def empty(cls, rows: int, cols: int, block_rows: int = 1, device=None):
-        torch = _torch()
+        torch = _T or _torch()
         if block_rows not in (1, 128) or rows < 0 or not 1 <= cols <= _lib.MUON_MAX_COLS8:
             raise ValueError("rows >= 0, cols in [1, MUON_MAX_COLS8], block_rows 1 or 128")
         t = cls.__new__(cls)
@@ -111,7 +134,7 @@ def _matrix(t, name: str):
 
 
 def _vector(t, n: int, name: str):
-    if t.dtype != _torch().float32 or t.shape != (n,) or not t.is_contiguous():
+    if t.dtype != (_T or _torch()).float32 or t.shape != (n,) or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous fp32 vector of {n} elements")
     return t.data_ptr()
 
@@ -127,22 +150,28 @@ def _device(first, *others) -> int:
     return index
 
 
-def _raw_stream(index: int) -> int:
-    torch = _torch()
-    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return get(index) if get else torch.cuda.current_stream(index).cuda_stream
-
-
 def _scratch(nbytes: int, index: int, workspace):
-    """(pointer, bytes) of the workspace.  The default one of a stream is used
-    there only, so that nothing has to be recorded when it is large enough."""
+    """(pointer, bytes, what keeps it) of the workspace.  The default one of a
+    stream is used there only, so that nothing has to be recorded when it is
+    large enough.  A call that is being captured takes its own from the graph's
+    memory instead: graphs captured on one stream may be replayed on several."""
     if nbytes == 0:
-        return 0, 0
+        return 0, 0, None
     if workspace is None:
-        kept = _default_ws.get((f"cuda:{index}", _raw_stream(index)))
+        torch = _T or _torch()
+        if torch.cuda.current_device() == index:
+            capturing = torch.cuda.is_current_stream_capturing()
+        else:
+            with torch.cuda.device(index):
+                capturing = torch.cuda.is_current_stream_capturing()
+        if capturing:
+            buf = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
+            return buf.data_ptr(), nbytes, buf
+        kept = _default_ws.get((f"cuda:{index}", _stream_of(index)))
         if kept is not None and kept.buf is not None and kept.buf.numel() >= nbytes:
-            return kept.buf.data_ptr(), kept.buf.numel()
-    return _workspace(nbytes, _torch().device("cuda", index), workspace)
+            return kept.buf.data_ptr(), kept.buf.numel(), kept.buf
+    ptr, size = _workspace(nbytes, (_T or _torch()).device("cuda", index), workspace)
+    return ptr, size, workspace
 
 
 def _tensor_of(workspace):
@@ -151,13 +180,13 @@ def _tensor_of(workspace):
 
 
 def _call(index: int, name: str, *args):
-    torch = _torch()
+    torch = _T or _torch()
     fn = getattr(lib(), name)
     if torch.cuda.current_device() == index:
-        st = fn(*args, _raw_stream(index))
+        st = fn(*args, _stream_of(index))
     else:
         with torch.cuda.device(index):
-            st = fn(*args, _raw_stream(index))
+            st = fn(*args, _stream_of(index))
     if st != MUON_OK:
         raise MuonError(st, name)
 
@@ -166,6 +195,7 @@ def quantize8(x, block_rows: int = 1, *, transposed: bool = False, out=None):
     """``x`` (rows, cols), bf16 or fp32, as a Tensor8.  With ``transposed``
     (128-row blocks only) returns (Tensor8 of x, Tensor8 of x^T): the same
     values and scales in both layouts, in one pass."""
+    _T or _torch()
     xp, rows, cols, ldx = _matrix(x, "x")
     code = _dtype_code(x.dtype)
     if transposed and block_rows != 128:
@@ -185,7 +215,7 @@ def quantize8(x, block_rows: int = 1, *, transposed: bool = False, out=None):
 
 def dequantize8(t, dtype=None):
     """The values of a Tensor8 as bf16 (default) or fp32, exact in both."""
-    torch = _torch()
+    torch = _T or _torch()
     dtype = dtype or torch.bfloat16
     code = _dtype_code(dtype)
     index = _device(t.data)
@@ -197,7 +227,7 @@ def dequantize8(t, dtype=None):
 def matmul8(a, b, *, out_dtype=None, out=None):
     """a b^T of two Tensor8, (m, k) and (n, k) -> (m, n) in bf16 (default) or
     fp32, sums in fp32.  ``out`` may have a row stride."""
-    torch = _torch()
+    torch = _T or _torch()
     if a.cols != b.cols:
         raise ValueError(f"a and b must have the same number of columns: {a.cols}, {b.cols}")
     index = _device(a.data, b.data, out)
@@ -221,7 +251,7 @@ def weight_grad(dy, x, *, out_dtype=None, out=None, accumulate: bool = False, wo
     """dy^T x: the gradient (n, k) of a linear layer's weights from its output
     gradient ``dy`` (tokens, n), bf16, and its input ``x``, a Tensor8 (tokens,
     k).  fp32 (default) or bf16; ``accumulate`` adds to an fp32 ``out``."""
-    torch = _torch()
+    torch = _T or _torch()
     dyp, tokens, n, lddy = _matrix(dy, "dy")
     k = x.cols
     if x.rows != tokens:
@@ -234,9 +264,11 @@ def weight_grad(dy, x, *, out_dtype=None, out=None, accumulate: bool = False, wo
     index = _device(dy, x.data, out, _tensor_of(workspace))
     if out is None:
         out = torch.empty(n, k, dtype=out_dtype or torch.float32, device=dy.device)
-    wptr, wbytes = _scratch(lib().muon_weight_grad_workspace_bytes(tokens, n, k), index, workspace)
+    wptr, wbytes, kept = _scratch(lib().muon_weight_grad_workspace_bytes(tokens, n, k), index,
+                                  workspace)
     _call(index, "muon_weight_grad", dyp, _dtype_code(dy.dtype), lddy, tokens, n, x._c,
           out.data_ptr(), _dtype_code(out.dtype), 1 if accumulate else 0, wptr, wbytes)
+    del kept  # until the launch
     return out
 
 
@@ -244,7 +276,7 @@ def layer_norm(x, weight, bias=None, *, eps: float = 1e-5, out_dtype=None):
     """Layer norm over the last axis of ``x`` (rows, cols): (y, mean, rstd).
     ``out_dtype`` bf16 or fp32 (default: x's), or torch.float8_e4m3fn for a
     Tensor8 with blocks of 1 x 128.  ``weight`` and ``bias`` are fp32."""
-    torch = _torch()
+    torch = _T or _torch()
     xp, rows, cols, ldx = _matrix(x, "x")
     wp = _vector(weight, cols, "weight")
     bp = _vector(bias, cols, "bias") if bias is not None else None
@@ -274,7 +306,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, bias: bool = True, dweight
     or the Tensor8 that was kept of it; dx has dy's dtype.  ``dweight`` and
     ``dbias`` (fp32) may be given, and are added to with ``accumulate``;
     ``bias`` False: no dbias (None)."""
-    torch = _torch()
+    torch = _T or _torch()
     dyp, rows, cols, lddy = _matrix(dy, "dy")
     if isinstance(x, Tensor8):
         same = x.shape == (rows, cols)
@@ -302,9 +334,10 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, bias: bool = True, dweight
     if bias and dbias is None:
         dbias = weight.new_empty(cols)
         dbp = dbias.data_ptr()
-    wptr, wbytes = _scratch(lib().muon_layer_norm_backward_workspace_bytes(rows, cols), index,
-                            workspace)
+    wptr, wbytes, kept = _scratch(lib().muon_layer_norm_backward_workspace_bytes(rows, cols),
+                                  index, workspace)
     _call(index, "muon_layer_norm_backward", dyp, _dtype_code(dy.dtype), lddy, xp, xcode, ldx,
           x8, rows, cols, wp, mp, rp, dx.data_ptr(), cols, dwp, dbp, 1 if accumulate else 0,
           wptr, wbytes)
+    del kept  # until the launch
     return dx, dweight, dbias

@@ -477,6 +477,40 @@ def test_layer_captured_replays_match_eager():
     del graph
 
 
+def test_two_graphs_replayed_at_once():
+    # both captured on one stream, with partial sums: each has its own scratch
+    announce("two graphs at once")
+    dy = [randn(9000, 300, seed=i, dtype=BF16) for i in (1, 2)]
+    x8 = [mn.quantize8(randn(9000, 260, seed=i)) for i in (3, 4)]
+    x, w, _ = norm_inputs(9000, 300, BF16)
+    _, mean, rstd = mn.layer_norm(x, w)
+    assert mn.weight_grad_workspace_bytes(9000, 300, 260) > 0
+
+    def both(i):
+        return (mn.weight_grad(dy[i], x8[i]),) + mn.layer_norm_backward(dy[i], x, w, mean, rstd)
+
+    want = [both(i) for i in (0, 1)]
+    graphs, got = [], []
+    for i in (0, 1):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(both(i))
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for replay in range(5):
+        for i in (0, 1):
+            for t in got[i]:
+                t.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            assert all(torch.equal(p, q) for p, q in zip(got[i], want[i])), (replay, i)
+    del graphs
+
+
 def test_two_streams_at_once():
     announce("two streams at once")
     want = [outputs_of(layer(*layer_inputs(t))) for t in (1500, 700)]

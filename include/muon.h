@@ -267,11 +267,12 @@ int muon_step_static(int n, const int* rows, const int* cols,
 typedef struct {
   void* data;     /* device, muon_tensor8_bytes(rows, cols) bytes, 16-byte aligned */
   void* scale;    /* device, muon_tensor8_scale_bytes(...) bytes, 4-byte aligned */
-  int rows, cols; /* rows >= 0, 1 <= cols <= MUON_MAX_COLS8 */
+  int rows, cols; /* 0 <= rows <= MUON_MAX_ROWS, 1 <= cols <= MUON_MAX_COLS8 */
   int block_rows; /* 1 or 128 */
 } muon_tensor8;
 
 #define MUON_MAX_COLS8 (1 << 22)
+#define MUON_MAX_ROWS 2147483392 /* 2^31 - 256: rows of any matrix of these calls */
 #define MUON_MAX_NORM_COLS 16384 /* longest row of a layer norm */
 
 /* Bytes of an 8-bit tensor's values and scales.  0 for rows == 0 or invalid sizes. */

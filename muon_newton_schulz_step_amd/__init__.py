@@ -26,7 +26,7 @@ from . import _lib
 from ._lib import (  # noqa: F401
     EXPORTS, KERNEL_KINDS, MUON_BF16, MUON_FP32, MUON_MAX_STEPS, MUON_OK, MUON_ERR_HIP,
     MUON_ERR_INVALID_ARG, MUON_ERR_UNSUPPORTED, MUON_ERR_WORKSPACE, MUON_STATIC_SCRATCH_BYTES,
-    MUON_MAX_COLS8, MUON_MAX_NORM_COLS,
+    MUON_MAX_COLS8, MUON_MAX_NORM_COLS, MUON_MAX_ROWS,
 )
 
 DEFAULT_EPS = 1e-7

@@ -14,6 +14,7 @@ MUON_WORKSPACE_ALIGN = 256
 MUON_PTR_ALIGN = 16
 MUON_STATIC_SCRATCH_BYTES = 256 << 20
 MUON_MAX_COLS8 = 1 << 22
+MUON_MAX_ROWS = 2 ** 31 - 256
 MUON_MAX_NORM_COLS = 16384
 KERNEL_KINDS = ("prep", "norm", "gram", "poly", "update", "final", "normuon", "apply",
                 "gramq", "quant8", "matmul8", "weight_grad", "layer_norm", "layer_norm_back")

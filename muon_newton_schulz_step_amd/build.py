@@ -22,9 +22,9 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libmuon.so")
 SOURCES = ["gemm_update.hip", "gemm_final_w.hip", "gemm_final_out.hip", "gemm_gram.hip",
            "gemm_poly.hip", "gemm_fp32.hip", "muon_kernels.hip", "muon_peaks.hip",
-           "muon_static.hip", "quantize8.hip", "layer_norm.hip", "matmul8.hip",
-           "weight_grad.hip",
-           "muon_api.cpp", "muon_layer.cpp"]
+           "muon_static.hip", "layers/quantize8.hip", "layers/layer_norm.hip",
+           "layers/matmul8.hip", "layers/weight_grad.hip",
+           "muon_api.cpp", "layers/muon_layer.cpp"]
 ARCH = os.environ.get("MUON_OFFLOAD_ARCH", "gfx950")
 
 
@@ -65,7 +65,8 @@ def _run(cmd):
 def build(verbose: bool = False, jobs: int | None = None) -> str:
     jobs = jobs or min(len(SOURCES), max(1, min(16, os.cpu_count() or 1)))
     with tempfile.TemporaryDirectory(prefix="muon_build_") as tmpdir:
-        objs = [os.path.join(tmpdir, os.path.splitext(s)[0] + ".o") for s in SOURCES]
+        objs = [os.path.join(tmpdir, os.path.splitext(os.path.basename(s))[0] + ".o")
+                for s in SOURCES]
         cmds = [compile_command(s, o) for s, o in zip(SOURCES, objs)]
         if verbose:
             for c in cmds:

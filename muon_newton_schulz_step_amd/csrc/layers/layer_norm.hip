@@ -6,6 +6,12 @@
 //             dw = sum over rows of dy xh, db = sum over rows of dy
 // All sums are fp32.  Both passes read each row once and are bound by HBM.
 //
+//   16384 x 1280 fp32 to bf16 23.7 us (5.3 TB/s), 8192 x 4096 bf16 24.4 us
+//   (5.5 TB/s); backward 8192 x 4096 bf16 39.8 us (5.1 TB/s) and 4.3 us for the
+//   reduction of 256 partial sums.  A 1 GiB copy runs at 5.2.
+// While a row is worked on, the team's next one is on its way (without: 30 us
+// forward and 64 us backward of 8192 x 4096).
+//
 // A team of TEAM waves holds a row in registers, 8 consecutive columns per
 // lane and chunk (a chunk: 512 columns per wave), so the mean and the sum of
 // squared deviations are two passes over registers, not over memory.  Teams

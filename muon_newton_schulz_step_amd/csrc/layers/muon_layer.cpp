@@ -43,12 +43,13 @@ bool conflict(std::initializer_list<Span> written, std::initializer_list<Span> r
 }
 
 bool shape8_ok(int rows, int cols, int block_rows) {
-  return rows >= 0 && cols >= 1 && cols <= MUON_MAX_COLS8 && (block_rows == 1 || block_rows == 128);
+  return rows >= 0 && rows <= MUON_MAX_ROWS && cols >= 1 && cols <= MUON_MAX_COLS8 && (block_rows == 1 || block_rows == 128);
 }
 // A matrix operand: sizes, stride, pointer.  Its rows must have a byte range
 // that a signed 64-bit offset reaches, which any real allocation has.
 bool matrix_ok(const void* p, int rows, int cols, long long ld) {
-  return rows >= 0 && cols >= 1 && ld >= cols && ld <= (1LL << 31) &&
+  return rows >= 0 && rows <= MUON_MAX_ROWS && cols >= 1 && cols <= MUON_MAX_ROWS && ld >= cols &&
+         ld <= (1LL << 31) &&
          (rows == 0 || (p && aligned(p, MUON_PTR_ALIGN)));
 }
 bool tensor8_ok(const muon_tensor8* t) {
@@ -65,7 +66,7 @@ int shift_of(const muon_tensor8* t) { return t->block_rows == 128 ? 7 : 0; }
 // Pieces of 512 columns, the element-wise kernels' unit of work, are counted
 // in 32 bits, and so are the tiles of a launch.
 bool pieces_fit(int rows, int cols) {
-  return (double)rows * (double)((cols + 511) / 512) < 4294967296.0;
+  return (double)rows * (double)((cols + 511LL) / 512) < 4294967040.0;
 }
 bool tiles_fit(long long rows, long long cols) {
   return (double)((rows + 63) / 64) * (double)((cols + 63) / 64) < 2147483648.0;
@@ -169,7 +170,9 @@ int muon_matmul8(const muon_tensor8* a, const muon_tensor8* b, void* y, int y_dt
 }
 
 size_t muon_weight_grad_workspace_bytes(int tokens, int n, int k) {
-  if (tokens < 0 || n < 1 || k < 1) return 0;
+  if (tokens < 0 || tokens > MUON_MAX_ROWS || n < 1 || n > MUON_MAX_ROWS || k < 1 ||
+      k > MUON_MAX_COLS8)
+    return 0;
   const int splits = weight_grad_plan(tokens, n, k).splits;
   return splits > 1 ? (size_t)splits * (size_t)n * (size_t)k * sizeof(float) : 0;
 }
@@ -256,7 +259,7 @@ int muon_layer_norm(const void* x, int x_dtype, long long ldx, int rows, int col
 }
 
 size_t muon_layer_norm_backward_workspace_bytes(int rows, int cols) {
-  if (rows < 1 || cols < 1 || cols > MUON_MAX_NORM_COLS) return 0;
+  if (rows < 1 || rows > MUON_MAX_ROWS || cols < 1 || cols > MUON_MAX_NORM_COLS) return 0;
   return norm_workspace(rows, cols);
 }
 

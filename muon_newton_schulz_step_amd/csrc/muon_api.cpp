@@ -17,9 +17,9 @@
 #include <mutex>
 #include <vector>
 
+#include "layers/muon_layer.h"
 #include "muon.h"
 #include "muon_kernels.h"
-#include "muon_layer.h"
 
 using namespace muon;
 

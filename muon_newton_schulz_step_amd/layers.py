@@ -63,9 +63,12 @@ class Tensor8:
     scale  (ceil(rows / block_rows), ceil(cols / 512) * 4) torch.uint8: the
            byte e + 127 of the scale 2^e
 
-    A value is its e4m3 number times its block's scale."""
+    A value is its e4m3 number times its block's scale.  The tensors may be
+    written in place, but not exchanged for others."""
 
-    __slots__ = ("data", "scale", "cols", "block_rows", "_c")
+    # one made by `empty` holds both in one allocation, and makes the two
+    # tensors when they are first asked for
+    __slots__ = ("_data", "_scale", "_buf", "_index", "_cols", "_block_rows", "_c")
 
     def __init__(self, data, scale, cols: int, block_rows: int = 1):
         torch = _T or _torch()
@@ -80,12 +83,11 @@ class Tensor8:
         rows = data.shape[0]
         if scale.shape != (-(-rows // block_rows), _scale_ld8(cols)) or not scale.is_contiguous():
             raise ValueError("scale must be contiguous, (blocks of rows, 4 ceil(cols / 512))")
-        if data.get_device() != scale.get_device():
+        index = data.get_device()
+        if scale.get_device() != index:
             raise ValueError("data and scale must be on one device")
-        self._set(data, scale, rows, cols, block_rows)
-
-    def _set(self, data, scale, rows, cols, block_rows):
-        self.data, self.scale, self.cols, self.block_rows = data, scale, cols, block_rows
+        self._data, self._scale, self._buf = data, scale, None
+        self._index, self._cols, self._block_rows = index, cols, block_rows
         self._c = _lib.MuonTensor8(data.data_ptr(), scale.data_ptr(), rows, cols, block_rows)
 
     @classmethod
@@ -94,22 +96,52 @@ class Tensor8:
         if block_rows not in (1, 128) or rows < 0 or not 1 <= cols <= _lib.MUON_MAX_COLS8:
             raise ValueError("rows >= 0, cols in [1, MUON_MAX_COLS8], block_rows 1 or 128")
         t = cls.__new__(cls)
-        t._set(torch.empty(rows, _ld8(cols), dtype=torch.float8_e4m3fn, device=device),
-               torch.empty(-(-rows // block_rows), _scale_ld8(cols), dtype=torch.uint8,
-                           device=device), rows, cols, block_rows)
+        nbytes = rows * _ld8(cols)
+        buf = torch.empty(nbytes + -(-rows // block_rows) * _scale_ld8(cols), dtype=torch.uint8,
+                          device=device)
+        t._data = t._scale = None
+        t._buf, t._index, t._cols, t._block_rows = buf, buf.get_device(), cols, block_rows
+        ptr = buf.data_ptr()
+        t._c = _lib.MuonTensor8(ptr, ptr + nbytes, rows, cols, block_rows)
         return t
 
     @property
+    def data(self):
+        if self._data is None:
+            rows, ld = self._c.rows, _ld8(self._cols)
+            self._data = self._buf[:rows * ld].view((_T or _torch()).float8_e4m3fn).view(rows, ld)
+        return self._data
+
+    @property
+    def scale(self):
+        if self._scale is None:
+            rows = self._c.rows
+            self._scale = self._buf[rows * _ld8(self._cols):].view(
+                -(-rows // self._block_rows), _scale_ld8(self._cols))
+        return self._scale
+
+    @property
+    def cols(self) -> int:
+        return self._cols
+
+    @property
+    def block_rows(self) -> int:
+        return self._block_rows
+
+    @property
     def rows(self) -> int:
-        return self.data.shape[0]
+        return self._c.rows
 
     @property
     def shape(self):
-        return (self.data.shape[0], self.cols)
+        return (self._c.rows, self._cols)
 
     @property
     def device(self):
-        return self.data.device
+        return (self._data if self._buf is None else self._buf).device
+
+    def get_device(self) -> int:
+        return self._index
 
     def dequantize(self, dtype=None):
         return dequantize8(self, dtype)
@@ -129,7 +161,8 @@ def _matrix(t, name: str):
         raise ValueError(f"{name} must have at least one column")
     ld, inner = t.stride()
     if (inner != 1 and cols > 1) or (ld < cols and rows > 1):
-        raise ValueError(f"{name}: elements of a row must be adjacent, and rows not overlap")
+        raise ValueError(f"{name}: elements of a row must be adjacent, and rows not overlap "
+                         "(an expanded or transposed tensor: contiguous() first)")
     return t.data_ptr(), rows, cols, ld if rows > 1 else cols
 
 
@@ -140,7 +173,7 @@ def _vector(t, n: int, name: str):
 
 
 def _device(first, *others) -> int:
-    """The index of the GPU that every tensor (None: no tensor) is on."""
+    """The index of the GPU that every tensor or Tensor8 (None: none) is on."""
     index = first.get_device()
     if index < 0:
         raise ValueError("tensors must be GPU tensors")
@@ -204,7 +237,7 @@ def quantize8(x, block_rows: int = 1, *, transposed: bool = False, out=None):
         raise ValueError("a tensor without rows has no transposed copy")
     if out is not None and (out.shape != (rows, cols) or out.block_rows != block_rows):
         raise ValueError("out must be a Tensor8 of x's shape and block_rows")
-    index = _device(x, out.data if out is not None else None)
+    index = _device(x, out)
     if out is None:
         out = Tensor8.empty(rows, cols, block_rows, x.device)
     other = Tensor8.empty(cols, rows, 128, x.device) if transposed else None
@@ -218,7 +251,7 @@ def dequantize8(t, dtype=None):
     torch = _T or _torch()
     dtype = dtype or torch.bfloat16
     code = _dtype_code(dtype)
-    index = _device(t.data)
+    index = _device(t)
     y = torch.empty(t.rows, t.cols, dtype=dtype, device=t.device)
     _call(index, "muon_dequantize8", t._c, y.data_ptr(), code, t.cols)
     return y
@@ -230,10 +263,10 @@ def matmul8(a, b, *, out_dtype=None, out=None):
     torch = _T or _torch()
     if a.cols != b.cols:
         raise ValueError(f"a and b must have the same number of columns: {a.cols}, {b.cols}")
-    index = _device(a.data, b.data, out)
-    m, n = a.data.shape[0], b.data.shape[0]
+    index = _device(a, b, out)
+    m, n = a.rows, b.rows
     if out is None:
-        out = torch.empty(m, n, dtype=out_dtype or torch.bfloat16, device=a.data.device)
+        out = torch.empty(m, n, dtype=out_dtype or torch.bfloat16, device=a.device)
         yp, ldy = out.data_ptr(), max(n, 1)
     else:
         if out.shape != (m, n) or (out_dtype or out.dtype) != out.dtype:
@@ -261,7 +294,7 @@ def weight_grad(dy, x, *, out_dtype=None, out=None, accumulate: bool = False, wo
     if out is not None and (out.shape != (n, k) or (out_dtype or out.dtype) != out.dtype
                             or not out.is_contiguous()):
         raise ValueError("out must be contiguous, (dy columns, x columns), and of out_dtype")
-    index = _device(dy, x.data, out, _tensor_of(workspace))
+    index = _device(dy, x, out, _tensor_of(workspace))
     if out is None:
         out = torch.empty(n, k, dtype=out_dtype or torch.float32, device=dy.device)
     wptr, wbytes, kept = _scratch(lib().muon_weight_grad_workspace_bytes(tokens, n, k), index,
@@ -310,11 +343,11 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, bias: bool = True, dweight
     dyp, rows, cols, lddy = _matrix(dy, "dy")
     if isinstance(x, Tensor8):
         same = x.shape == (rows, cols)
-        xp, xcode, ldx, x8, xt = None, MUON_BF16, cols, x._c, x.data
+        xp, xcode, ldx, x8 = None, MUON_BF16, cols, x._c
     else:
         same = x.shape == dy.shape
         xp, _, _, ldx = _matrix(x, "x")
-        xcode, x8, xt = _dtype_code(x.dtype), None, x
+        xcode, x8 = _dtype_code(x.dtype), None
     if not same:
         raise ValueError("x and dy must have the same shape")
     if not bias and dbias is not None:
@@ -325,7 +358,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, bias: bool = True, dweight
     mp, rp = _vector(mean, rows, "mean"), _vector(rstd, rows, "rstd")
     dwp = _vector(dweight, cols, "dweight") if dweight is not None else 0
     dbp = _vector(dbias, cols, "dbias") if dbias is not None else None
-    index = _device(dy, xt, weight, mean, rstd, dweight, dbias, _tensor_of(workspace))
+    index = _device(dy, x, weight, mean, rstd, dweight, dbias, _tensor_of(workspace))
     device = dy.device
     dx = torch.empty(rows, cols, dtype=dy.dtype, device=device)
     if dweight is None:

@@ -27,6 +27,7 @@ def t8(k, rows=8, cols=256, block_rows=1, data=None, scale=None):
     (1, 1, 1, 128, 4), (3, 128, 1, 384, 12), (3, 129, 128, 768, 4), (129, 513, 128, 129 * 640, 16),
     (5, 1283, 1, 5 * 1408, 5 * 12), (0, 128, 1, 0, 0), (8, 0, 1, 0, 0), (-1, 8, 1, 0, 0),
     (1 << 30, 1 << 22, 1, 1 << 52, 1 << 45), (1, (1 << 22) + 1, 1, 0, 0),
+    (2 ** 31 - 256, 1, 1, (2 ** 31 - 256) * 128, (2 ** 31 - 256) * 4), (2 ** 31 - 255, 1, 1, 0, 0),
 ])
 def test_sizes(rows, cols, block_rows, data, scale):
     lib = mn.lib()
@@ -43,6 +44,7 @@ def quantize(x=P, dtype=BF16, rows=8, cols=256, ldx=256, out=None, other=None):
 @pytest.mark.parametrize("kw,expect", [
     (dict(dtype=2), INVALID), (dict(x=0), INVALID), (dict(x=P + 2), INVALID),
     (dict(rows=-1), INVALID), (dict(cols=0), INVALID), (dict(ldx=255), INVALID),
+    (dict(rows=2 ** 31 - 255, out=t8(1, 2 ** 31 - 255)), INVALID),
     (dict(rows=7), INVALID), (dict(cols=255), INVALID),          # not the output's shape
     (dict(out=t8(1, block_rows=64)), INVALID), (dict(out=t8(1, data=0)), INVALID),
     (dict(out=t8(1, scale=0)), INVALID), (dict(out=t8(1, data=P * 64 + 8)), INVALID),
@@ -113,7 +115,8 @@ def test_workspace_sizes():
     assert mn.weight_grad_workspace_bytes(0, 48, 256) == 0
     assert mn.layer_norm_backward_workspace_bytes(5, 768) % (2 * 768 * 4) == 0
     assert mn.layer_norm_backward_workspace_bytes(5, 768) > 0
-    for bad in ((0, 768), (5, 0), (5, mn.MUON_MAX_NORM_COLS + 1)):
+    assert mn.weight_grad_workspace_bytes(2 ** 31 - 255, 48, 256) == 0
+    for bad in ((0, 768), (5, 0), (5, mn.MUON_MAX_NORM_COLS + 1), (2 ** 31 - 255, 768)):
         assert mn.layer_norm_backward_workspace_bytes(*bad) == 0
 
 
@@ -168,6 +171,8 @@ def test_tensor8_checks():
     t = mn.Tensor8(data, scale, 300)
     assert t.shape == (5, 300) and t.rows == 5 and "5 x 300" in repr(t)
     assert mn.Tensor8.empty(130, 300, 128).scale.shape == (2, 4)
+    with pytest.raises(AttributeError):
+        t.data = data
     for bad in (lambda: mn.Tensor8(data, scale, 200), lambda: mn.Tensor8(data, scale, 385),
                 lambda: mn.Tensor8(data, scale, 0), lambda: mn.Tensor8(data, scale, 300, 2),
                 lambda: mn.Tensor8(data, scale, 300, 128), lambda: mn.Tensor8(data[:4], scale, 300),

@@ -327,7 +327,8 @@ int muon_layer_norm(const void* x, int x_dtype, long long ldx, int rows, int col
  * that was kept of it (rows x cols); exactly one of the two.  dy and dx: bf16 or
  * fp32, the same type.  dweight, dbias: fp32, cols elements, added to with
  * accumulate; dbias may be NULL.  workspace:
- * muon_layer_norm_backward_workspace_bytes, MUON_WORKSPACE_ALIGN-aligned. */
+ * muon_layer_norm_backward_workspace_bytes, possibly 0 (then it may be NULL),
+ * MUON_WORKSPACE_ALIGN-aligned. */
 size_t muon_layer_norm_backward_workspace_bytes(int rows, int cols);
 int muon_layer_norm_backward(const void* dy, int dy_dtype, long long lddy, const void* x,
                              int x_dtype, long long ldx, const muon_tensor8* x8, int rows,

@@ -235,12 +235,21 @@ __global__ __launch_bounds__(64 * back_waves(TEAM)) void layer_norm_back_kernel(
   }
   // the workgroup's sums: every team's go to LDS (element i of a chunk's lanes
   // side by side, the rows of 64 padded by one, so that neither the writes nor
-  // the reads meet in a bank) and are added in the teams' order
+  // the reads meet in a bank) and are added in the teams' order.  A single
+  // workgroup's are the result, others are partial sums.
+  const bool last = gridDim.x == 1;
   float* part = a.part + (long long)blockIdx.x * 2 * a.cols;
+  auto put = [&](float* out, float* sums_of, int c, float s) __attribute__((always_inline)) {
+    if (!last)
+      sums_of[c] = s;
+    else if (out)
+      out[c] = a.accumulate ? out[c] + s : s;
+  };
   if constexpr (TEAMS > 1) {
     constexpr int ROW = 65, PER = NCH * TEAM * 8 * ROW;
     __shared__ float acc[TEAMS * PER];
-    auto join = [&](const float (&v)[NCH][8], float* out) __attribute__((always_inline)) {
+    auto join = [&](const float (&v)[NCH][8], float* out, float* sums_of)
+                    __attribute__((always_inline)) {
 #pragma unroll
       for (int k = 0; k < NCH; ++k)
 #pragma unroll
@@ -252,18 +261,21 @@ __global__ __launch_bounds__(64 * back_waves(TEAM)) void layer_norm_back_kernel(
         float s = acc[at];
 #pragma unroll
         for (int t = 1; t < TEAMS; ++t) s += acc[t * PER + at];
-        out[c] = s;
+        put(out, sums_of, c, s);
       }
       __syncthreads();
     };
-    join(dw, part);
-    join(db, part + a.cols);
+    join(dw, a.dweight, part);
+    join(db, a.dbias, part + a.cols);
   } else {
 #pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      store8_edge(part + col[k], a.cols - col[k], dw[k]);
-      store8_edge(part + a.cols + col[k], a.cols - col[k], db[k]);
-    }
+    for (int k = 0; k < NCH; ++k)
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (col[k] + i < a.cols) {
+          put(a.dweight, part, col[k] + i, dw[k][i]);
+          put(a.dbias, part + a.cols, col[k] + i, db[k][i]);
+        }
   }
 }
 
@@ -317,12 +329,15 @@ int groups_for(int rows, int teams, int most) {
 }  // namespace
 
 // Workgroups of the backward pass, each with one partial sum: one per CU, which
-// holds a CU's share of the registers and keeps the partial sums few.
+// holds a CU's share of the registers and keeps the partial sums few.  Up to two
+// rows to a team one workgroup does it all, without partial sums and a second
+// launch.
 int norm_backward_groups(int rows, int cols) {
   int g = 0;
   with_shape(cols, [&](auto team, auto) {
     constexpr int T = decltype(team)::value;
-    g = groups_for(rows, back_waves(T) / T, 256);
+    constexpr int teams = back_waves(T) / T;
+    g = rows > 0 && rows <= 2 * teams ? 1 : groups_for(rows, teams, 256);
   });
   return g;
 }
@@ -370,7 +385,7 @@ hipError_t launch_layer_norm_backward(int dy_bf16, int x, const NormBackArgs& a,
       go(std::integral_constant<int, MUON_FP32>{});
   });
   hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
+  if (err != hipSuccess || a.groups == 1) return err;
   hipLaunchKernelGGL(norm_reduce_kernel, dim3((a.cols + 31) / 32, a.dbias ? 2 : 1), dim3(1024), 0,
                      s, a.part, a.groups, a.cols, a.dweight, a.dbias, a.accumulate);
   return hipGetLastError();

@@ -74,7 +74,8 @@ bool tiles_fit(long long rows, long long cols) {
 int status_of(hipError_t e) { return e == hipSuccess ? MUON_OK : MUON_ERR_HIP; }
 
 size_t norm_workspace(int rows, int cols) {
-  return (size_t)norm_backward_groups(rows, cols) * 2 * (size_t)cols * sizeof(float);
+  const int groups = norm_backward_groups(rows, cols);
+  return groups > 1 ? (size_t)groups * 2 * (size_t)cols * sizeof(float) : 0;
 }
 
 }  // namespace
@@ -292,8 +293,7 @@ int muon_layer_norm_backward(const void* dy, int dy_dtype, long long lddy, const
                {s_dy, in, in_s, Span{weight, vec}, Span{mean, per_row}, Span{rstd, per_row}}))
     return MUON_ERR_INVALID_ARG;
   if (cols > MUON_MAX_NORM_COLS) return MUON_ERR_UNSUPPORTED;
-  if (rows > 0) {
-    const size_t need = norm_workspace(rows, cols);
+  if (const size_t need = norm_workspace(rows, cols)) {
     if (!workspace || workspace_bytes < need || !aligned(workspace, MUON_WORKSPACE_ALIGN))
       return MUON_ERR_WORKSPACE;
     if (conflict({Span{workspace, need}},

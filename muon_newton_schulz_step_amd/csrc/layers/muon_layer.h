@@ -117,7 +117,7 @@ struct NormBackArgs {
   float* dweight;
   float* dbias;             // or null
   int accumulate;
-  float* part;              // [groups][2][cols]
+  float* part;              // [groups][2][cols], unused with one group
   int groups;
 };
 int norm_backward_groups(int rows, int cols);

@@ -113,8 +113,9 @@ def test_workspace_sizes():
     need = mn.weight_grad_workspace_bytes(1 << 14, 48, 256)
     assert need > 0 and need % (48 * 256 * 4) == 0
     assert mn.weight_grad_workspace_bytes(0, 48, 256) == 0
-    assert mn.layer_norm_backward_workspace_bytes(5, 768) % (2 * 768 * 4) == 0
-    assert mn.layer_norm_backward_workspace_bytes(5, 768) > 0
+    assert mn.layer_norm_backward_workspace_bytes(500, 768) % (2 * 768 * 4) == 0
+    assert mn.layer_norm_backward_workspace_bytes(500, 768) > 0
+    assert mn.layer_norm_backward_workspace_bytes(1, 768) == 0
     assert mn.weight_grad_workspace_bytes(2 ** 31 - 255, 48, 256) == 0
     for bad in ((0, 768), (5, 0), (5, mn.MUON_MAX_NORM_COLS + 1), (2 ** 31 - 255, 768)):
         assert mn.layer_norm_backward_workspace_bytes(*bad) == 0
@@ -142,7 +143,7 @@ def test_layer_norm_refusals(kw, expect):
     assert norm(**kw) == expect
 
 
-def norm_back(dy=P, dtype=BF16, lddy=256, x=P * 2, x_dtype=BF16, ldx=256, x8=None, rows=8, cols=256,
+def norm_back(dy=P, dtype=BF16, lddy=256, x=P * 2, x_dtype=BF16, ldx=256, x8=None, rows=800, cols=256,
               w=P * 3, mean=P * 4, rstd=P * 5, dx=P * 6, lddx=256, dw=P * 7, db=P * 8, accumulate=0,
               ws=P * 9, ws_bytes=P):
     return mn.lib().muon_layer_norm_backward(dy, dtype, lddy, x, x_dtype, ldx, x8, rows, cols, w,
@@ -152,13 +153,14 @@ def norm_back(dy=P, dtype=BF16, lddy=256, x=P * 2, x_dtype=BF16, ldx=256, x8=Non
 
 @pytest.mark.parametrize("kw,expect", [
     (dict(dtype=2), INVALID), (dict(x_dtype=2), INVALID), (dict(dy=0), INVALID), (dict(x=0), INVALID),
-    (dict(x8=t8(1)), INVALID), (dict(x=0, x8=t8(1, 7)), INVALID), (dict(x=0, x8=t8(1, cols=255)), INVALID),
+    (dict(x8=t8(1, 800)), INVALID), (dict(x=0, x8=t8(1, 7)), INVALID),
+    (dict(x=0, x8=t8(1, 800, 255)), INVALID),
     (dict(dx=0), INVALID), (dict(dx=P), INVALID), (dict(dx=P * 2), INVALID), (dict(lddx=255), INVALID),
     (dict(w=0), INVALID), (dict(dw=0), INVALID), (dict(dw=P * 3), INVALID), (dict(db=P * 7), INVALID),
     (dict(mean=0), INVALID), (dict(accumulate=-1), INVALID), (dict(dw=P * 7 + 2), INVALID),
     (dict(ws=0), WORKSPACE), (dict(ws_bytes=64), WORKSPACE), (dict(ws=P * 9 + 16), WORKSPACE),
     (dict(ws=P * 7), INVALID),
-    (dict(cols=16385, lddy=16385, ldx=16385, lddx=16385), UNSUPPORTED),
+    (dict(rows=8, cols=16385, lddy=16385, ldx=16385, lddx=16385), UNSUPPORTED),
     (dict(rows=0, accumulate=1), mn.MUON_OK),
 ])
 def test_layer_norm_backward_refusals(kw, expect):

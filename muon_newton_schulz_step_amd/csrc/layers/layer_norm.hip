@@ -163,6 +163,8 @@ template <int DT, int XT, int TEAM, int NCH>
 __global__ __launch_bounds__(64 * back_waves(TEAM)) void layer_norm_back_kernel(NormBackArgs a) {
   using D = typename ElemOf<DT>::type;
   constexpr int WAVES = back_waves(TEAM), TEAMS = WAVES / TEAM;
+  // the next row does not fit the registers beside four chunks of fp32
+  constexpr bool EARLY = NCH < 4 || (DT != MUON_FP32 && XT != MUON_FP32);
   __shared__ float sums[2][TEAMS][2][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int tw = wave % TEAM, team = wave / TEAM;
@@ -191,11 +193,12 @@ __global__ __launch_bounds__(64 * back_waves(TEAM)) void layer_norm_back_kernel(
   };
   int turn = 0;
   long long first = (long long)blockIdx.x * TEAMS;  // of the workgroup's teams
-  if (first + team < a.rows) fetch(first + team);
+  if (EARLY && first + team < a.rows) fetch(first + team);
   for (; first < a.rows; first += step) {
     const long long row = first + team;
     const bool in = row < a.rows;
     float x[NCH][8], d[NCH][8];
+    if (!EARLY && in) fetch(row);
     const float mu = mu_next, r = r_next;
     float s[2] = {0.f, 0.f};
     if (in) {
@@ -204,7 +207,7 @@ __global__ __launch_bounds__(64 * back_waves(TEAM)) void layer_norm_back_kernel(
         rx[k].get(x[k]);
         rd[k].get(d[k]);
       }
-      if (row + step < a.rows) fetch(row + step);
+      if (EARLY && row + step < a.rows) fetch(row + step);
 #pragma unroll
       for (int k = 0; k < NCH; ++k)
 #pragma unroll
@@ -268,14 +271,24 @@ __global__ __launch_bounds__(64 * back_waves(TEAM)) void layer_norm_back_kernel(
     join(dw, a.dweight, part);
     join(db, a.dbias, part + a.cols);
   } else {
+    auto store = [&](float (&v)[8], float* out, float* sums_of, int c)
+                     __attribute__((always_inline)) {
+      if (!last) {
+        store8_edge(sums_of + c, a.cols - c, v);
+      } else if (out) {
+        float old[8];
+        load8_edge(out + c, a.accumulate ? a.cols - c : 0, old);
+        if (a.accumulate)
 #pragma unroll
-    for (int k = 0; k < NCH; ++k)
+          for (int i = 0; i < 8; ++i) v[i] = old[i] + v[i];
+        store8_edge(out + c, a.cols - c, v);
+      }
+    };
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (col[k] + i < a.cols) {
-          put(a.dweight, part, col[k] + i, dw[k][i]);
-          put(a.dbias, part + a.cols, col[k] + i, db[k][i]);
-        }
+    for (int k = 0; k < NCH; ++k) {
+      store(dw[k], a.dweight, part, col[k]);
+      store(db[k], a.dbias, part + a.cols, col[k]);
+    }
   }
 }
 
@@ -304,19 +317,21 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* part, in
 }
 
 namespace {
-// Team and chunks for a row of `cols` columns: one wave up to 2048, four up to
-// 8192, eight up to 16384; the fewest chunks that hold the row.
-template <typename F>
+// Team and chunks for a row of `cols` columns.  Forward: one wave up to 2048,
+// four up to 8192, eight up to 16384; the fewest chunks that hold the row.
+// Backward: at most three chunks to a lane, where the team can be larger
+// instead, since four with their gradient sums spill in fp32 (16000 x 8192 fp32,
+// four waves of four chunks: 720 us; eight of two: 198 us).
+template <bool BACK, typename F>
 void with_shape(int cols, F&& f) {
-  auto go = [&](auto team, auto nch) { f(team, nch); };
-#define MUON_SHAPE(T, N) go(std::integral_constant<int, T>{}, std::integral_constant<int, N>{})
+#define MUON_SHAPE(T, N) f(std::integral_constant<int, T>{}, std::integral_constant<int, N>{})
   if (cols <= 512) MUON_SHAPE(1, 1);
   else if (cols <= 1024) MUON_SHAPE(1, 2);
   else if (cols <= 1536) MUON_SHAPE(1, 3);
-  else if (cols <= 2048) MUON_SHAPE(1, 4);
+  else if (cols <= 2048) MUON_SHAPE(BACK ? 2 : 1, BACK ? 2 : 4);
   else if (cols <= 4096) MUON_SHAPE(4, 2);
   else if (cols <= 6144) MUON_SHAPE(4, 3);
-  else if (cols <= 8192) MUON_SHAPE(4, 4);
+  else if (cols <= 8192) MUON_SHAPE(BACK ? 8 : 4, BACK ? 2 : 4);
   else if (cols <= 12288) MUON_SHAPE(8, 3);
   else MUON_SHAPE(8, 4);
 #undef MUON_SHAPE
@@ -334,7 +349,7 @@ int groups_for(int rows, int teams, int most) {
 // launch.
 int norm_backward_groups(int rows, int cols) {
   int g = 0;
-  with_shape(cols, [&](auto team, auto) {
+  with_shape<true>(cols, [&](auto team, auto) {
     constexpr int T = decltype(team)::value;
     constexpr int teams = back_waves(T) / T;
     g = rows > 0 && rows <= 2 * teams ? 1 : groups_for(rows, teams, 256);
@@ -343,7 +358,7 @@ int norm_backward_groups(int rows, int cols) {
 }
 
 hipError_t launch_layer_norm(int x_bf16, int out, const NormArgs& a, hipStream_t s) {
-  with_shape(a.cols, [&](auto team, auto nch) {
+  with_shape<false>(a.cols, [&](auto team, auto nch) {
     constexpr int T = decltype(team)::value, N = decltype(nch)::value;
     const dim3 grid(groups_for(a.rows, T > 4 ? 1 : 4 / T, T > 4 ? 512 : 2048)),
         block(T > 4 ? 64 * T : 256);
@@ -367,7 +382,7 @@ hipError_t launch_layer_norm(int x_bf16, int out, const NormArgs& a, hipStream_t
 }
 
 hipError_t launch_layer_norm_backward(int dy_bf16, int x, const NormBackArgs& a, hipStream_t s) {
-  if (a.groups > 0) with_shape(a.cols, [&](auto team, auto nch) {
+  if (a.groups > 0) with_shape<true>(a.cols, [&](auto team, auto nch) {
     constexpr int T = decltype(team)::value, N = decltype(nch)::value;
     const dim3 grid(a.groups), block(64 * back_waves(T));
     auto go = [&](auto dt) {

@@ -399,27 +399,28 @@ void go(const Matmul8Args& a, hipStream_t s) {
       hipLaunchKernelGGL((matmul8_rows_kernel<2, 2, Y>), grid, block, 0, s, a);
     return;
   }
-  // The tile by the time of the fullest CU, in us per k-tile.  Measured: 256 x
-  // 256 (one per CU) 1.55; 128 x 128 0.72 alone and 0.88 for two; 64 x 64 0.30
-  // alone, and 0.2 for each of several beside 0.1.  (512 x 4096 x 4096: 38, 21, 18
-  // us with the three tiles; 2048 x 2048 x 2048: 23.5, 11.6, 14.9 us; 6000 x 2000 x
-  // 700: 15.1, 17.5, 21.5 us.)  A result in fp32 has no 256 x 256 tile: with the
-  // operands' bf16 forms it does not fit the registers.
+  // The tile by the time of the fullest CU, in us per k-tile.  Measured, for a
+  // result in bf16: 256 x 256 (one per CU) 1.55; 128 x 128 0.72 alone and 0.88 for
+  // two; 64 x 64 0.30 alone, and 0.2 for each of several beside 0.1.  (512 x 4096
+  // x 4096: 38, 21, 18 us with the three tiles; 2048 x 2048 x 2048: 23.5, 11.6,
+  // 14.9 us; 6000 x 2000 x 700: 15.1, 17.5, 21.5 us.)  In fp32: 3.3; 1.05 and 1.8;
+  // 0.39 and 0.34 each (8192 x 4096 x 4096: 213, 229 us with the first two; 6000 x
+  // 2000 x 700: 26.8, 23.5 us; 512 x 4096 x 4096: 36.3, 26.6 us with the last two).
+  constexpr bool FP32 = std::is_same_v<Y, float>;
   auto share = [&](int bm, int bn) {  // tiles of the fullest CU
     return (double)(((long long)((a.m + bm - 1) / bm) * ((a.n + bn - 1) / bn) + 255) / 256);
   };
   const double q256 = share(256, 256), q128 = share(128, 128), q64 = share(64, 64);
-  const double t256 = 1.55 * q256;
-  const double t128 = q128 == 1 ? 0.72 : 0.44 * q128 + ((long long)q128 % 2 ? 0.28 : 0.0);
-  const double t64 = q64 == 1 ? 0.3 : 0.1 + 0.2 * q64;
-  constexpr bool FP32 = std::is_same_v<Y, float>;
-  if (t64 < t128 && (FP32 || t64 < t256)) {
+  const double odd = (long long)q128 % 2 ? 1.0 : 0.0;
+  const double t256 = (FP32 ? 3.3 : 1.55) * q256;
+  const double t128 = FP32 ? 0.9 * q128 + 0.15 * odd : 0.44 * q128 + 0.28 * odd;
+  const double t64 = FP32 ? 0.05 + 0.34 * q64 : 0.1 + 0.2 * q64;
+  if (t64 < t128 && t64 < t256)
     tiles<64, 64, 2, 1, Y>(a, s);
-  } else if (FP32 || t128 < t256) {
+  else if (t128 < t256)
     tiles<128, 128, 2, 2, Y>(a, s);
-  } else if constexpr (!FP32) {
+  else
     tiles<256, 256, 4, 2, Y>(a, s);
-  }
 }
 }  // namespace
 

@@ -165,6 +165,10 @@ def test_matmul8_large_grids(m, n, k):
     product_case(m, n, k, 1, 128, BF16)
 
 
+def test_matmul8_large_grid_fp32():
+    product_case(8190, 4100, 1283, 1, 128, FP32)
+
+
 def test_matmul8_row_stride_and_non_finite():
     announce("matmul8 strided output, NaN rows")
     for m in (3, 70, 200):

@@ -19,6 +19,7 @@
 namespace muon {
 
 constexpr int kTileT = 64;  // tokens per LDS tile
+constexpr int kGroupN = 4;
 
 // Wait until this wave has no LDS operation in flight (lgkmcnt(0), the other
 // counters untouched: loads into registers stay in flight).
@@ -42,7 +43,8 @@ __device__ __forceinline__ void wait_lgkm0() {
 // MFMA comes its share of the substep's LDS reads and writes.
 // Token tiles below the ragged edges are loaded without a branch, in line with
 // the MFMAs.
-//   8192 tokens, 4096 x 4096, 256 x 256 tiles: 220 us, 1.25 PFLOP/s (393 us
+//   8192 tokens, 4096 x 4096, 256 x 256 tiles: 220 to 230 us by box, 1.19 to
+//   1.25 PFLOP/s (393 us
 //   with 128 x 128 tiles on 4 waves, everything loaded and stored at the tile's
 //   ends, and no order pinned; 234 us with a branch around each load; a
 //   library's plain bf16 product of 8192^3 runs at 1.41).  The MFMAs are busy
@@ -66,7 +68,13 @@ __global__ __launch_bounds__(64 * WGN * WGK) void weight_grad_kernel(WeightGradA
   const int L = xcd_remap((int)blockIdx.x, (int)gridDim.x);
   const int tiles = g.tiles_n * g.tiles_k;
   const int split = L / tiles, tile = L - split * tiles;
-  const int n0 = tile / g.tiles_k * BN, k0 = tile % g.tiles_k * BK;
+  // Tiles go in groups of kGroupN tile rows, column by column: an XCD's 32 CUs
+  // then share 4 panels of dy and 8 of x, not 2 and 16 (16384 tokens, 4096 x
+  // 16384: 1805 -> 1782 us; 8192 tokens, 4096 x 4096: 231 -> 230).
+  const int group = tile / (kGroupN * g.tiles_k), first = group * kGroupN;
+  const int rows = g.tiles_n - first < kGroupN ? g.tiles_n - first : kGroupN;
+  const int place = tile - first * g.tiles_k;
+  const int n0 = (first + place % rows) * BN, k0 = place / rows * BK;
   const int t_first = split * g.tiles_per_split;
   const int t_all = (g.tokens + kTileT - 1) / kTileT;
   const int t_end = t_first + g.tiles_per_split < t_all ? t_first + g.tiles_per_split : t_all;

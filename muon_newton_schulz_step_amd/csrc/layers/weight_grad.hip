@@ -44,12 +44,12 @@ __device__ __forceinline__ void wait_lgkm0() {
 // Token tiles below the ragged edges are loaded without a branch, in line with
 // the MFMAs.
 //   8192 tokens, 4096 x 4096, 256 x 256 tiles: 220 to 230 us by box, 1.19 to
-//   1.25 PFLOP/s (393 us
-//   with 128 x 128 tiles on 4 waves, everything loaded and stored at the tile's
-//   ends, and no order pinned; 234 us with a branch around each load; a
-//   library's plain bf16 product of 8192^3 runs at 1.41).  The MFMAs are busy
-//   half the time, the LDS a third; neither reading operands two substeps ahead
-//   nor loading two token tiles ahead changed that.
+//   1.25 PFLOP/s (393 us with 128 x 128 tiles on 4 waves, everything loaded and
+//   stored at the tile's ends, and no order pinned; 234 us with a branch around
+//   each load; a library's plain bf16 product of 8192^3 runs at 1.36 to 1.41).
+//   The MFMAs are busy 56% of the cycles, at 1.92 GHz, the LDS a third; neither
+//   reading operands two substeps ahead nor loading two token tiles ahead
+//   changed that.
 
 template <int BN, int BK, int WGN, int WGK, typename W>
 __global__ __launch_bounds__(64 * WGN * WGK) void weight_grad_kernel(WeightGradArgs g) {

@@ -91,10 +91,12 @@ __global__ __launch_bounds__(64 * WGN * WGK) void weight_grad_kernel(WeightGradA
   u32x2_t rx[PK];
   int sx[PK];
   // A chunk past dy's or x's last column reads the tile's first one, and one
-  // across dy's last column reads into the next row: what comes of them is not
-  // stored.  Only the last row has no next one, and rows past it must be zero:
-  // from token tile `safe` on, loads look at each chunk.
-  const int safe = n_all ? g.tokens / kTileT : (g.tokens - 1) / kTileT;
+  // across dy's last column reads up to 7 elements behind it, of the rows that
+  // follow: what comes of them is not stored.  The last row has none that follow
+  // (nor, where rows are shorter than 7, have the last 7), and rows past it
+  // must be zero: from token tile `safe` on, loads look at each chunk.
+  const int short_rows = n_all ? 0 : g.lddy < 7 ? 7 : 1;
+  const int safe = g.tokens > short_rows ? (g.tokens - short_rows) / kTileT : 0;
   auto gload = [&](int kt, auto plain) __attribute__((always_inline)) {
     const int t0 = kt * kTileT;
     const bf16_t* dyb = static_cast<const bf16_t*>(g.dy) + (long long)t0 * g.lddy + n0;

@@ -233,6 +233,19 @@ def test_weight_grad_strided_and_128_row_blocks():
 
 def test_weight_grad_keeps_non_finite_rows_apart():
     announce("weight_grad NaN")
+@pytest.mark.parametrize("n", [1, 2, 3, 6, 7, 9])
+def test_weight_grad_short_rows(n):
+    # the last rows of dy are shorter than a vector of 8; what lies behind dy
+    # has no part in the result
+    for tokens in (64, 70, 129, 1000):
+        announce(f"weight_grad short rows {tokens} {n}")
+        buf = torch.full((tokens * n + 64,), float("nan"), dtype=BF16, device=DEV)
+        dy = buf[:tokens * n].view(tokens, n).copy_(randn(tokens, n, seed=n))
+        x = mn.quantize8(randn(tokens, 140, seed=tokens))
+        d, v = to64(dy), parts(x)[2]
+        within(mn.weight_grad(dy, x), d.T @ v, 2 * U * (tokens + 2) * (np.abs(d).T @ np.abs(v)))
+
+
     dy, x = randn(130, 40, seed=1, dtype=BF16), randn(130, 50, seed=2)
     x[129, 3], dy[0, 7] = float("nan"), float("inf")
     dw = mn.weight_grad(dy, mn.quantize8(x))

@@ -282,7 +282,8 @@ size_t muon_tensor8_scale_bytes(int rows, int cols, int block_rows);
 /* x (rows x cols, bf16 or fp32) as an 8-bit tensor, and with `transposed` (a
  * cols x rows tensor with block_rows 128; NULL: none) its transposed copy with
  * the same values and scales, which needs out->block_rows == 128.
- * MUON_ERR_UNSUPPORTED for a transposed copy of 1-row blocks. */
+ * MUON_ERR_UNSUPPORTED for a transposed copy of 1-row blocks, and, as for
+ * muon_dequantize8, for rows * ceil(cols / 512) above 2^28 - 16. */
 int muon_quantize8(const void* x, int x_dtype, int rows, int cols, long long ldx,
                    const muon_tensor8* out, const muon_tensor8* transposed, hipStream_t stream);
 
@@ -291,16 +292,19 @@ int muon_dequantize8(const muon_tensor8* t, void* y, int y_dtype, long long ldy,
                      hipStream_t stream);
 
 /* y = a b^T for a (m x k) and b (n x k), y m x n in bf16 or fp32, sums in
- * fp32.  Either operand may have either kind of block. */
+ * fp32.  Either operand may have either kind of block.  For a bf16 result of
+ * many rows the matrix instruction cuts each product off 13 bits below the
+ * largest of its group of 8 along k (about 1.5e-5 of the result's norm, far
+ * below the rounding to bf16); fp32 results come from exact products. */
 int muon_matmul8(const muon_tensor8* a, const muon_tensor8* b, void* y, int y_dtype,
                  long long ldy, hipStream_t stream);
 
 /* dw = dy^T x, or with accumulate dw += dy^T x: the gradient of W (n x k,
  * dense, as muon_step takes it) from the layer's output gradient dy (tokens x
  * n, bf16, lddy <= 2^26; fp32 and longer strides return MUON_ERR_UNSUPPORTED)
- * and its input x (tokens x k) kept in 8 bits.  Sums in fp32.  dw is fp32 or bf16; accumulating into bf16
- * returns MUON_ERR_UNSUPPORTED (every addition would be rounded to 8 bits of
- * mantissa).  The workspace (muon_weight_grad_workspace_bytes, possibly 0, then
+ * and its input x (tokens x k) kept in 8 bits.  Sums in fp32.  dw is fp32 or
+ * bf16; accumulating into bf16 returns MUON_ERR_UNSUPPORTED (every addition
+ * would be rounded to 8 bits of mantissa).  The workspace (muon_weight_grad_workspace_bytes, possibly 0, then
  * it may be NULL) holds partial sums. */
 size_t muon_weight_grad_workspace_bytes(int tokens, int n, int k);
 int muon_weight_grad(const void* dy, int dy_dtype, long long lddy, int tokens, int n,

@@ -390,8 +390,9 @@ void go(const Matmul8Args& a, hipStream_t s) {
   // enough rows share the second half's saving (16 x 8192 x 4096: 11.1 -> 8.7 us,
   // 32 x 8192 x 4096: 16.6 -> 11.7 us; but 1 x 8192 x 8192: 13 -> 20 us, 16 x 8192
   // x 8192: 20 -> 22 us).  Past 16 rows a very wide product is faster in tiles (32
-  // x 16384 x 4096: 22.8 -> 17.6 us).
-  if (a.m <= 16 || (a.m <= 32 && a.n < 16384)) {
+  // x 16384 x 4096: 22.8 -> 17.6 us).  A workgroup of 512 threads for 16 columns
+  // reaches the 2^32 threads of a launch at 2^27 columns: tiles from there on.
+  if ((a.m <= 16 && a.n <= (1 << 26)) || (a.m <= 32 && a.n < 16384)) {
     const dim3 block(64 * kFewWaves);
     const bool two = a.n >= 8192 && (a.m > 16 || (a.m > 8 && a.ld <= 4096));
     const dim3 grid(two ? (a.n + 31) / 32 : (a.n + 15) / 16);

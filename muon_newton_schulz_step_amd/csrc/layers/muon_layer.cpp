@@ -63,10 +63,10 @@ Span scale_of(const muon_tensor8* t) {
 }
 unsigned char* bytes_of(void* p) { return static_cast<unsigned char*>(p); }
 int shift_of(const muon_tensor8* t) { return t->block_rows == 128 ? 7 : 0; }
-// Pieces of 512 columns, the element-wise kernels' unit of work, are counted
-// in 32 bits, and so are the tiles of a launch.
+// Pieces of 512 columns, the element-wise kernels' unit of work, have 16 threads
+// each, and a launch has less than 2^32.  Tiles are counted in 32 bits.
 bool pieces_fit(int rows, int cols) {
-  return (double)rows * (double)((cols + 511LL) / 512) < 4294967040.0;
+  return (double)rows * (double)((cols + 511LL) / 512) <= 268435440.0;
 }
 bool tiles_fit(long long rows, long long cols) {
   return (double)((rows + 63) / 64) * (double)((cols + 63) / 64) < 2147483648.0;

@@ -19,8 +19,9 @@ from __future__ import annotations
 import ctypes
 
 from . import _lib
-from . import (MUON_BF16, MUON_FP32, MUON_OK, MuonError, Workspace, _default_ws, _workspace,
-               lib)
+from . import MUON_BF16, MUON_FP32, MUON_OK, MuonError, Workspace, lib
+
+_MAX_ROWS = _lib.MUON_MAX_ROWS
 
 # torch, its raw stream query and the element types' codes, from the first call on
 _T = None
@@ -81,6 +82,8 @@ class Tensor8:
         if data.dim() != 2 or data.shape[1] != _ld8(cols) or not data.is_contiguous():
             raise ValueError("data must be contiguous, (rows, cols rounded up to 128)")
         rows = data.shape[0]
+        if rows > _lib.MUON_MAX_ROWS:
+            raise ValueError(f"at most {_lib.MUON_MAX_ROWS} rows")
         if scale.shape != (-(-rows // block_rows), _scale_ld8(cols)) or not scale.is_contiguous():
             raise ValueError("scale must be contiguous, (blocks of rows, 4 ceil(cols / 512))")
         index = data.get_device()
@@ -93,8 +96,10 @@ class Tensor8:
     @classmethod
     def empty(cls, rows: int, cols: int, block_rows: int = 1, device=None):
         torch = _T or _torch()
-        if block_rows not in (1, 128) or rows < 0 or not 1 <= cols <= _lib.MUON_MAX_COLS8:
-            raise ValueError("rows >= 0, cols in [1, MUON_MAX_COLS8], block_rows 1 or 128")
+        if (block_rows not in (1, 128) or not 0 <= rows <= _lib.MUON_MAX_ROWS
+                or not 1 <= cols <= _lib.MUON_MAX_COLS8):
+            raise ValueError("rows in [0, MUON_MAX_ROWS], cols in [1, MUON_MAX_COLS8], "
+                             "block_rows 1 or 128")
         t = cls.__new__(cls)
         nbytes = rows * _ld8(cols)
         buf = torch.empty(nbytes + -(-rows // block_rows) * _scale_ld8(cols), dtype=torch.uint8,
@@ -159,6 +164,8 @@ def _matrix(t, name: str):
     rows, cols = t.shape
     if cols < 1:
         raise ValueError(f"{name} must have at least one column")
+    if rows > _MAX_ROWS or cols > _MAX_ROWS:  # the C ABI's sizes are 32-bit
+        raise ValueError(f"{name} has more than {_MAX_ROWS} rows or columns")
     ld, inner = t.stride()
     if (inner != 1 and cols > 1) or (ld < cols and rows > 1):
         raise ValueError(f"{name}: elements of a row must be adjacent, and rows not overlap "

@@ -580,6 +580,22 @@ def test_offsets_past_32_bits():
     dy[-3:] = randn(3, 8, seed=3).bfloat16()
     dw = mn.weight_grad(dy, t)
     d = to64(dy[-3:])
+def test_one_row_by_more_columns_than_a_launch_has_threads_for():
+    announce("matmul8 of one row, 2^27 + 70 columns")
+    n = (1 << 27) + 70
+    b = mn.Tensor8.empty(n, 128, device=DEV)
+    b.data.view(torch.uint8).zero_()
+    b.scale.fill_(127)
+    tail = mn.quantize8(randn(70, 128, seed=1))
+    b.data.view(torch.uint8)[-70:] = tail.data.view(torch.uint8)
+    b.scale[-70:] = tail.scale
+    a = mn.quantize8(randn(1, 128, seed=2))
+    y = mn.matmul8(a, b, out_dtype=FP32)
+    av, bv = parts(a)[2], parts(tail)[2]
+    within(y[:, -70:].contiguous(), av @ bv.T, 2 * U * 129 * (np.abs(av) @ np.abs(bv).T))
+    assert torch.count_nonzero(y[:, :-70]) == 0
+
+
     within(dw, d.T @ av, 2 * U * (rows + 2) * (np.abs(d).T @ np.abs(av)))
     del t, y, dw
     announce("offsets past 32 bits: layer_norm")

@@ -212,6 +212,27 @@ def test_binding_refuses_host_tensors_and_shapes():
         mn.dequantize8(t, torch.float16)
 
 
+@pytest.mark.parametrize("rows,cols", [(2 ** 28 - 15, 512), (2 ** 27, 513)])
+def test_more_threads_than_a_launch_has_are_refused(rows, cols):
+    # (pieces of 512 columns with 16 threads each)
+    far = t8(0, rows, cols, data=1 << 55, scale=1 << 57)
+    assert quantize(rows=rows, cols=cols, ldx=cols, out=far) == UNSUPPORTED
+    assert mn.lib().muon_dequantize8(far, P, BF16, cols, None) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("rows", [2 ** 31 - 255, 2 ** 32 + 5])
+def test_binding_refuses_rows_past_32_bits(rows):
+    # the sizes of the C ABI are ints: 2^32 + 5 rows must not pass for 5
+    x = torch.empty(rows, 1, dtype=torch.bfloat16, device="meta")
+    for bad in (lambda: mn.quantize8(x), lambda: mn.quantize8(x.t().contiguous()),
+                lambda: mn.layer_norm(x, torch.ones(1)),
+                lambda: mn.Tensor8.empty(rows, 1, device="meta"),
+                lambda: mn.Tensor8(torch.empty(rows, 128, dtype=torch.float8_e4m3fn, device="meta"),
+                                   torch.empty(rows, 4, dtype=torch.uint8, device="meta"), 1)):
+        with pytest.raises(ValueError, match="rows"):
+            bad()
+
+
 def test_oracle_rounding_pins():
     # e4m3: 3 fraction bits, normal from 2^-6, step 2^-9 below, largest 448
     table = np.array([s * f * 2.0 ** e for s in (1, -1) for e in range(-6, 9)

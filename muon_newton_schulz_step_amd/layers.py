@@ -16,7 +16,7 @@ step of its weights:
 """
 from __future__ import annotations
 
-import ctypes
+import threading
 
 from . import _lib
 from . import MUON_BF16, MUON_FP32, MUON_OK, MuonError, Workspace, lib
@@ -190,15 +190,21 @@ def _device(first, *others) -> int:
     return index
 
 
+# The default workspaces of the calls here, one per (device, stream).  A call
+# that has one is two launches, which another thread's on the same stream (a
+# backward pass runs in a thread of its own) must not come between: it holds the
+# lock from before it takes the workspace until both are enqueued.
+_workspaces: dict = {}
+_lock = threading.Lock()
+
+
 def _scratch(nbytes: int, index: int, workspace):
     """(pointer, bytes, what keeps it) of the workspace.  The default one of a
     stream is used there only, so that nothing has to be recorded when it is
     large enough.  A call that is being captured takes its own from the graph's
     memory instead: graphs captured on one stream may be replayed on several."""
-    if nbytes == 0:
-        return 0, 0, None
+    torch = _T or _torch()
     if workspace is None:
-        torch = _T or _torch()
         if torch.cuda.current_device() == index:
             capturing = torch.cuda.is_current_stream_capturing()
         else:
@@ -207,11 +213,16 @@ def _scratch(nbytes: int, index: int, workspace):
         if capturing:
             buf = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
             return buf.data_ptr(), nbytes, buf
-        kept = _default_ws.get((f"cuda:{index}", _stream_of(index)))
-        if kept is not None and kept.buf is not None and kept.buf.numel() >= nbytes:
-            return kept.buf.data_ptr(), kept.buf.numel(), kept.buf
-    ptr, size = _workspace(nbytes, (_T or _torch()).device("cuda", index), workspace)
-    return ptr, size, workspace
+        key = (index, _stream_of(index))
+        workspace = _workspaces.get(key)
+        if workspace is None:
+            workspace = _workspaces[key] = Workspace()
+        buf = workspace.buf
+        if buf is not None and buf.numel() >= nbytes:
+            return buf.data_ptr(), buf.numel(), buf
+    if isinstance(workspace, Workspace):
+        workspace = workspace.get(nbytes, torch.device("cuda", index))
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
 def _tensor_of(workspace):
@@ -229,6 +240,16 @@ def _call(index: int, name: str, *args):
             st = fn(*args, _stream_of(index))
     if st != MUON_OK:
         raise MuonError(st, name)
+
+
+def _call_with_scratch(index: int, name: str, nbytes: int, workspace, *args):
+    if nbytes == 0:
+        _call(index, name, *args, 0, 0)
+        return
+    with _lock:
+        ptr, size, kept = _scratch(nbytes, index, workspace)
+        _call(index, name, *args, ptr, size)
+        del kept  # until the launches
 
 
 def quantize8(x, block_rows: int = 1, *, transposed: bool = False, out=None):
@@ -304,11 +325,9 @@ def weight_grad(dy, x, *, out_dtype=None, out=None, accumulate: bool = False, wo
     index = _device(dy, x, out, _tensor_of(workspace))
     if out is None:
         out = torch.empty(n, k, dtype=out_dtype or torch.float32, device=dy.device)
-    wptr, wbytes, kept = _scratch(lib().muon_weight_grad_workspace_bytes(tokens, n, k), index,
-                                  workspace)
-    _call(index, "muon_weight_grad", dyp, _dtype_code(dy.dtype), lddy, tokens, n, x._c,
-          out.data_ptr(), _dtype_code(out.dtype), 1 if accumulate else 0, wptr, wbytes)
-    del kept  # until the launch
+    _call_with_scratch(index, "muon_weight_grad", lib().muon_weight_grad_workspace_bytes(tokens, n, k),
+                       workspace, dyp, _dtype_code(dy.dtype), lddy, tokens, n, x._c, out.data_ptr(),
+                       _dtype_code(out.dtype), 1 if accumulate else 0)
     return out
 
 
@@ -374,10 +393,8 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, bias: bool = True, dweight
     if bias and dbias is None:
         dbias = weight.new_empty(cols)
         dbp = dbias.data_ptr()
-    wptr, wbytes, kept = _scratch(lib().muon_layer_norm_backward_workspace_bytes(rows, cols),
-                                  index, workspace)
-    _call(index, "muon_layer_norm_backward", dyp, _dtype_code(dy.dtype), lddy, xp, xcode, ldx,
-          x8, rows, cols, wp, mp, rp, dx.data_ptr(), cols, dwp, dbp, 1 if accumulate else 0,
-          wptr, wbytes)
-    del kept  # until the launch
+    _call_with_scratch(index, "muon_layer_norm_backward",
+                       lib().muon_layer_norm_backward_workspace_bytes(rows, cols), workspace, dyp,
+                       _dtype_code(dy.dtype), lddy, xp, xcode, ldx, x8, rows, cols, wp, mp, rp,
+                       dx.data_ptr(), cols, dwp, dbp, 1 if accumulate else 0)
     return dx, dweight, dbias

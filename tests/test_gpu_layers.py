@@ -9,6 +9,8 @@ instruction that cuts each product off 13 bits below the largest of its
 group of 8 (measured on the chip, see CUT8).  Values taken from 8 bits are exact in fp32
 and bf16, and so are products of two of them.  Quantisation has no bound: its
 result is one number, and it has to be that one."""
+import concurrent.futures
+
 import numpy as np
 import pytest
 import torch
@@ -231,8 +233,6 @@ def test_weight_grad_strided_and_128_row_blocks():
     assert torch.equal(mn.weight_grad(whole[:, 8:108], x), mn.weight_grad(whole[:, 8:108].contiguous(), x))
 
 
-def test_weight_grad_keeps_non_finite_rows_apart():
-    announce("weight_grad NaN")
 @pytest.mark.parametrize("n", [1, 2, 3, 6, 7, 9])
 def test_weight_grad_short_rows(n):
     # the last rows of dy are shorter than a vector of 8; what lies behind dy
@@ -246,6 +246,8 @@ def test_weight_grad_short_rows(n):
         within(mn.weight_grad(dy, x), d.T @ v, 2 * U * (tokens + 2) * (np.abs(d).T @ np.abs(v)))
 
 
+def test_weight_grad_keeps_non_finite_rows_apart():
+    announce("weight_grad NaN")
     dy, x = randn(130, 40, seed=1, dtype=BF16), randn(130, 50, seed=2)
     x[129, 3], dy[0, 7] = float("nan"), float("inf")
     dw = mn.weight_grad(dy, mn.quantize8(x))
@@ -544,6 +546,28 @@ def test_two_streams_at_once():
             assert torch.equal(p, q)
 
 
+def test_two_threads_on_one_stream():
+    # calls of two launches that share the stream's scratch
+    announce("two threads on one stream")
+    dy = [randn(9000, 130, seed=i, dtype=BF16) for i in (1, 2)]
+    x8 = [mn.quantize8(randn(9000, 260, seed=i)) for i in (3, 4)]
+    x, w, _ = norm_inputs(9000, 130, BF16)
+    _, mean, rstd = mn.layer_norm(x, w)
+
+    def both(i):
+        return (mn.weight_grad(dy[i], x8[i]),) + mn.layer_norm_backward(dy[i], x, w, mean, rstd)
+
+    want = [both(i) for i in (0, 1)]
+    torch.cuda.synchronize()
+    with concurrent.futures.ThreadPoolExecutor(2) as pool:
+        runs = [pool.submit(lambda i: [both(i) for _ in range(50)], i) for i in (0, 1)]
+        got = [r.result(timeout=60) for r in runs]
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for g in got[i]:
+            assert all(torch.equal(p, q) for p, q in zip(g, want[i]))
+
+
 def test_timing_log_names_the_launches():
     announce("timing log")
     mn.timing_read()
@@ -554,6 +578,22 @@ def test_timing_log_names_the_launches():
     assert kinds.count("quant8") == 3 and kinds.count("matmul8") == 2
     assert kinds.count("weight_grad") == 2
     assert kinds.count("layer_norm") == kinds.count("layer_norm_back") == 1
+
+
+def test_one_row_by_more_columns_than_a_launch_has_threads_for():
+    announce("matmul8 of one row, 2^27 + 70 columns")
+    n = (1 << 27) + 70
+    b = mn.Tensor8.empty(n, 128, device=DEV)
+    b.data.view(torch.uint8).zero_()
+    b.scale.fill_(127)
+    tail = mn.quantize8(randn(70, 128, seed=1))
+    b.data.view(torch.uint8)[-70:] = tail.data.view(torch.uint8)
+    b.scale[-70:] = tail.scale
+    a = mn.quantize8(randn(1, 128, seed=2))
+    y = mn.matmul8(a, b, out_dtype=FP32)
+    av, bv = parts(a)[2], parts(tail)[2]
+    within(y[:, -70:].contiguous(), av @ bv.T, 2 * U * 129 * (np.abs(av) @ np.abs(bv).T))
+    assert torch.count_nonzero(y[:, :-70]) == 0
 
 
 def test_offsets_past_32_bits():
@@ -580,22 +620,6 @@ def test_offsets_past_32_bits():
     dy[-3:] = randn(3, 8, seed=3).bfloat16()
     dw = mn.weight_grad(dy, t)
     d = to64(dy[-3:])
-def test_one_row_by_more_columns_than_a_launch_has_threads_for():
-    announce("matmul8 of one row, 2^27 + 70 columns")
-    n = (1 << 27) + 70
-    b = mn.Tensor8.empty(n, 128, device=DEV)
-    b.data.view(torch.uint8).zero_()
-    b.scale.fill_(127)
-    tail = mn.quantize8(randn(70, 128, seed=1))
-    b.data.view(torch.uint8)[-70:] = tail.data.view(torch.uint8)
-    b.scale[-70:] = tail.scale
-    a = mn.quantize8(randn(1, 128, seed=2))
-    y = mn.matmul8(a, b, out_dtype=FP32)
-    av, bv = parts(a)[2], parts(tail)[2]
-    within(y[:, -70:].contiguous(), av @ bv.T, 2 * U * 129 * (np.abs(av) @ np.abs(bv).T))
-    assert torch.count_nonzero(y[:, :-70]) == 0
-
-
     within(dw, d.T @ av, 2 * U * (rows + 2) * (np.abs(d).T @ np.abs(av)))
     del t, y, dw
     announce("offsets past 32 bits: layer_norm")

@@ -49,8 +49,6 @@ __device__ __forceinline__ void team_sum(float (&v)[N], float (*buf)[16], int wa
   }
 }
 
-// Rows beyond the last one: a team without a row still takes part in the
-// workgroup's barriers.
 template <int XT, int OUT, int TEAM, int NCH>
 __global__ __launch_bounds__(TEAM > 4 ? 64 * TEAM : 256) void layer_norm_kernel(NormArgs a) {
   using X = typename ElemOf<XT>::type;
@@ -159,6 +157,7 @@ struct RawX<kOut8> {
 
 constexpr int back_waves(int team) { return team > 8 ? team : 8; }
 
+// A team without a row left still takes part in the workgroup's barriers.
 template <int DT, int XT, int TEAM, int NCH>
 __global__ __launch_bounds__(64 * back_waves(TEAM)) void layer_norm_back_kernel(NormBackArgs a) {
   using D = typename ElemOf<DT>::type;

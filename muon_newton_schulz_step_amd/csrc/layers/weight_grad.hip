@@ -304,21 +304,23 @@ __global__ __launch_bounds__(256) void weight_grad_join_kernel(const float* part
 }
 
 // The tile and the number of token splits.  A CU holds one workgroup of 256 x
-// 256 or 256 x 128 tiles, or two of 128 x 128 ones, all of 8 waves.  Measured per
-// token tile: 1.7 us (256 x 256), 0.95 us (256 x 128), and for 128 x 128
-// 0.55 us alone on its CU, 1.23 us for two.  The result and its parts move at
-// about 4.7 TB/s, written and read, and a second launch costs about 3 us.  The
-// plan takes the smallest sum.  (4096 tokens, 1280 x 5120: 62 us with 256 x
-// 128, 104 and 78 us with the others, these two before their loads went in line;
-// 16384 tokens, 768 x 1024: 38.5 us in 10 parts of 256 x 128, 40.5 us in 5 of
-// 128 x 128; 8192 tokens, 4096 x 4096: 220, 257, 314 us.)
+// 256 or 256 x 128 tiles, or two of 128 x 128 ones, all of 8 waves.  Per token
+// tile: 1.7 us (256 x 256), 1.05 us (256 x 128), and for 128 x 128 0.7 us alone
+// on its CU, 1.3 us for two.  The result and its parts move at 6 TB/s, written
+// and read, and a second launch costs 5 us.  The plan takes the smallest sum.
+// The constants are fitted to every tile and up to 32 parts at 33 sizes of 2048 to
+// 16384 tokens and 500 x 500 to 4096 x 4096: the plan's choice is within 5.3% of
+// the fastest at each and 0.4% on average.  (16384 tokens, 2048 x 2048: 143 us in
+// 4 parts of 256 x 256, 155 in 2 of 256 x 128, 158 with 128 x 128; 16384 tokens, 768
+// x 1003: 40.8 us in 10 parts of 256 x 128, 42.9 in 5 of 128 x 128; 2048 tokens,
+// 2048 x 2048: 26.9 us with 128 x 128, 34.1 with 256 x 128.)
 WeightGradPlan weight_grad_plan(int tokens, int n, int k) {
   struct Kind {
     int bn, bk, per_cu;
     double one, full;  // us per token tile: alone on its CU, all places taken
   };
   static const Kind kinds[3] = {
-      {256, 256, 1, 1.7, 1.7}, {256, 128, 1, 0.95, 0.95}, {128, 128, 2, 0.55, 1.23}};
+      {256, 256, 1, 1.7, 1.7}, {256, 128, 1, 1.05, 1.05}, {128, 128, 2, 0.7, 1.3}};
   const int tt = (int)(((long long)tokens + kTileT - 1) / kTileT);
   WeightGradPlan best{};
   double least = 0.0;
@@ -334,7 +336,7 @@ WeightGradPlan weight_grad_plan(int tokens, int n, int k) {
       const double us_tile = wgs <= 256 ? c.one : c.full;
       const double rounds = (double)((wgs + 256 * c.per_cu - 1) / (256 * c.per_cu));
       double us = rounds * per * us_tile;
-      if (splits > 1) us += 3.0 + 2.0 * splits * 4.0 * n * k / 4.7e6;
+      if (splits > 1) us += 5.0 + 2.0 * splits * 4.0 * n * k / 6e6;
       if (best.splits == 0 || us < least) {
         least = us;
         best = WeightGradPlan{i, splits, per, c.bn, c.bk};

@@ -67,9 +67,12 @@ __global__ __launch_bounds__(64 * WGM * WGN) void matmul8_tile_kernel(Matmul8Arg
   constexpr int CPR = 8;
   constexpr int B_CHUNKS = BN * CPR, STAGE = (BM + BN) * CPR;
   constexpr int DPW = STAGE / 64 / NW;      // loads of a wave per k-tile
-  constexpr int SPW = (BM + BN) / 64 / NW;  // and of scale words per four
+  // and of 64 scale words per four; where there are more waves than those, the
+  // others load the same again
+  constexpr int SG = (BM + BN) / 64, SPW = SG > NW ? SG / NW : 1;
   static_assert(DPW * 64 * NW == STAGE && B_CHUNKS % (DPW * 64) == 0, "one operand per wave");
-  static_assert(SPW * 64 * NW == BM + BN && BN % (SPW * 64) == 0, "one operand's scales per wave");
+  static_assert((SG % NW == 0 || NW % SG == 0) && BN % (SPW * 64) == 0,
+                "one operand's scales per wave");
   // the epilogue's staging: 32 rows m of half the wave's columns, per wave
   static_assert(FN % 2 == 0 && NW * 32 * (WTN / 2) * 4 <= STAGE * 16, "staging fits");
   __shared__ u32x4_t S0[STAGE], S1[STAGE];
@@ -102,21 +105,23 @@ __global__ __launch_bounds__(64 * WGM * WGN) void matmul8_tile_kernel(Matmul8Arg
     for (int d = 0; d < DPW; ++d) buffer_load_lds16(rs, voff[d], St + (wave_s * DPW + d) * 64);
   };
   // word w of the scales of the tile's rows: b's, then a's
-  const bool sc_b = wave_s * SPW * 64 < BN;
+  const int sg = SG < NW ? wave_s % SG : wave_s * SPW;
+  const bool sc_b = sg * 64 < BN;
   const int s_first = sc_b ? n0 : m0, s_last = sc_b ? g.n - 1 : g.m - 1;
   const int s_shift = sc_b ? g.shift_b : g.shift_a;
   const unsigned char* sbase = (sc_b ? g.sb : g.sa) + (long long)(s_first >> s_shift) * g.sld;
   unsigned soff[SPW];
 #pragma unroll
   for (int d = 0; d < SPW; ++d) {
-    const int i = (wave * SPW + d) * 64 + lane, r = s_first + (sc_b ? i : i - BN);
+    const int i = ((SG < NW ? wave % SG : wave * SPW) + d) * 64 + lane;
+    const int r = s_first + (sc_b ? i : i - BN);
     soff[d] = (unsigned)(((r < s_last ? r : s_last) >> s_shift) - (s_first >> s_shift)) *
               (unsigned)g.sld;
   }
   auto issue_scales = [&](int w, unsigned* C) __attribute__((always_inline)) {
     const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(sbase + 4 * (w < last_word ? w : last_word));
 #pragma unroll
-    for (int d = 0; d < SPW; ++d) buffer_load_lds4(rs, soff[d], C + (wave_s * SPW + d) * 64);
+    for (int d = 0; d < SPW; ++d) buffer_load_lds4(rs, soff[d], C + (sg + d) * 64);
   };
 
   f32x16_t acc[FN][FM];
@@ -410,9 +415,14 @@ void go(const Matmul8Args& a, hipStream_t s) {
   // result in bf16: 256 x 256 (one per CU) 1.55; 128 x 128 0.72 alone and 0.88 for
   // two; 64 x 64 0.30 alone, and 0.2 for each of several beside 0.1.  (512 x 4096
   // x 4096: 38, 21, 18 us with the three tiles; 2048 x 2048 x 2048: 23.5, 11.6,
-  // 14.9 us; 6000 x 2000 x 700: 15.1, 17.5, 21.5 us.)  In fp32: 3.3; 1.05 and 1.8;
-  // 0.39 and 0.34 each (8192 x 4096 x 4096: 213, 229 us with the first two; 6000 x
-  // 2000 x 700: 26.8, 23.5 us; 512 x 4096 x 4096: 36.3, 26.6 us with the last two).
+  // 14.9 us; 6000 x 2000 x 700: 15.1, 17.5, 21.5 us.)  In fp32: 3.3; 1.1 and 1.8;
+  // 0.56, and 0.265 each beside 0.3; its 128 x 128 tiles have 8 waves, which hide
+  // the conversions better (2048 x 1280 x 5120: 46.6 -> 37.2 us).  (8192 x 4096 x
+  // 4096: 217, 234, 275 us; 1024 x 4096 x 4096: 83, 36.2, 37.3 us; 2048 x 1280 x
+  // 1280: 31.6, 13.7, 12.7 us.)  Over 64 sizes of 48 to 16384 rows, 700 to 16384
+  // columns and sums of 700 to 5120 the choice is on average within 0.3% of the
+  // fastest of the three for either type (worst: 16384 x 5120 x 1280 in fp32,
+  // whose stores bound it, 273 us against 232).
   constexpr bool FP32 = std::is_same_v<Y, float>;
   auto share = [&](int bm, int bn) {  // tiles of the fullest CU
     return (double)(((long long)((a.m + bm - 1) / bm) * ((a.n + bn - 1) / bn) + 255) / 256);
@@ -420,12 +430,12 @@ void go(const Matmul8Args& a, hipStream_t s) {
   const double q256 = share(256, 256), q128 = share(128, 128), q64 = share(64, 64);
   const double odd = (long long)q128 % 2 ? 1.0 : 0.0;
   const double t256 = (FP32 ? 3.3 : 1.55) * q256;
-  const double t128 = FP32 ? 0.9 * q128 + 0.15 * odd : 0.44 * q128 + 0.28 * odd;
-  const double t64 = FP32 ? 0.05 + 0.34 * q64 : 0.1 + 0.2 * q64;
+  const double t128 = FP32 ? 0.9 * q128 + 0.2 * odd : 0.44 * q128 + 0.28 * odd;
+  const double t64 = FP32 ? 0.3 + 0.265 * q64 : 0.1 + 0.2 * q64;
   if (t64 < t128 && t64 < t256)
     tiles<64, 64, 2, 1, Y>(a, s);
   else if (t128 < t256)
-    tiles<128, 128, 2, 2, Y>(a, s);
+    tiles<128, 128, FP32 ? 4 : 2, 2, Y>(a, s);
   else
     tiles<256, 256, 4, 2, Y>(a, s);
 }

@@ -53,8 +53,9 @@ __device__ __forceinline__ i32x8_t frag8(const u32x4_t& lo, const u32x4_t& hi) {
 // one load.  Between the barrier and the next wait the wave has priority over
 // its neighbour, so that the two waves of a SIMD fall out of step and one's
 // MFMAs cover the other's waits (16384 x 16384 x 4096: 874 -> 822 us).
-//   256 x 256 tiles on 8 waves, inputs in the caches: 8192 x 4096 x 4096 103 us
-//   (2.67 PFLOP/s), 16384 x 16384 x 4096 788 us (2.80), to fp32 219 us and 1.25.
+//   256 x 256 tiles on 8 waves, inputs in the caches: 8192 x 4096 x 4096 103 to
+//   110 us by box (2.5 to 2.67 PFLOP/s), 16384 x 16384 x 4096 788 to 798 us (2.75
+//   to 2.80), to fp32 216 and 1766 us (1.25).
 //   A library's product with one scale per tensor runs at 2.72 to 2.80.  At the
 //   larger size the MFMAs are busy 70% of the cycles and the chip runs at 1.68
 //   GHz: it is bound by power.  Without the stores of y it would take 752 us.

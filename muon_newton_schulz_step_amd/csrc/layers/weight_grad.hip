@@ -43,11 +43,11 @@ __device__ __forceinline__ void wait_lgkm0() {
 // MFMA comes its share of the substep's LDS reads and writes.
 // Token tiles below the ragged edges are loaded without a branch, in line with
 // the MFMAs.
-//   8192 tokens, 4096 x 4096, 256 x 256 tiles: 220 to 230 us by box, 1.19 to
+//   8192 tokens, 4096 x 4096, 256 x 256 tiles: 220 to 236 us by box, 1.16 to
 //   1.25 PFLOP/s (393 us with 128 x 128 tiles on 4 waves, everything loaded and
 //   stored at the tile's ends, and no order pinned; 234 us with a branch around
 //   each load; a library's plain bf16 product of 8192^3 runs at 1.36 to 1.41).
-//   The MFMAs are busy 56% of the cycles, at 1.92 GHz, the LDS a third; neither
+//   The MFMAs are busy 59% of the cycles, at 1.96 GHz, the LDS a third; neither
 //   reading operands two substeps ahead nor loading two token tiles ahead
 //   changed that.
 

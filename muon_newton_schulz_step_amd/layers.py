@@ -13,6 +13,8 @@ step of its weights:
     dx, dg, db = layer_norm_backward(dh, x, g, mean, rstd)
     dW = weight_grad(dy, h8)                 # or out=dW, accumulate=True
     step([W], [dW], [buf], mu=0.95, lr=0.02)
+
+The backward passes are calls of their own: autograd records none of these.
 """
 from __future__ import annotations
 
@@ -23,19 +25,22 @@ from . import MUON_BF16, MUON_FP32, MUON_OK, MuonError, Workspace, lib
 
 _MAX_ROWS = _lib.MUON_MAX_ROWS
 
-# torch, its raw stream query and the element types' codes, from the first call on
+# torch, its raw stream and device queries and the element types' codes, from
+# the first call on, and the library's functions
 _T = None
-_stream_of = None
+_stream_of = _current_device = None
 _codes: dict = {}
+_functions: dict = {}
 
 
 def _torch():
-    global _T, _stream_of
+    global _T, _stream_of, _current_device
     if _T is None:
         import torch
         _codes.update({torch.bfloat16: MUON_BF16, torch.float32: MUON_FP32})
         _stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _T = torch
     return _T
 
@@ -205,7 +210,7 @@ def _scratch(nbytes: int, index: int, workspace):
     memory instead: graphs captured on one stream may be replayed on several."""
     torch = _T or _torch()
     if workspace is None:
-        if torch.cuda.current_device() == index:
+        if _current_device() == index:
             capturing = torch.cuda.is_current_stream_capturing()
         else:
             with torch.cuda.device(index):
@@ -231,12 +236,13 @@ def _tensor_of(workspace):
 
 
 def _call(index: int, name: str, *args):
-    torch = _T or _torch()
-    fn = getattr(lib(), name)
-    if torch.cuda.current_device() == index:
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(lib(), name)
+    if _current_device() == index:
         st = fn(*args, _stream_of(index))
     else:
-        with torch.cuda.device(index):
+        with _T.cuda.device(index):
             st = fn(*args, _stream_of(index))
     if st != MUON_OK:
         raise MuonError(st, name)

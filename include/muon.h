@@ -260,10 +260,11 @@ int muon_step_static(int n, const int* rows, const int* cols,
  * 4 bytes (the padding is not used).  A value is its e4m3 number times its
  * block's scale.  The library writes e = the smallest integer >= -117 such
  * that no finite value of the block exceeds 448 * 2^e in magnitude, and rounds
- * x / 2^e to nearest even; infinities and NaN become NaN and do not affect
- * the scale.  A power of two costs no precision, and every value is exact
- * in bf16.  Scales made elsewhere must have bytes 10 to 247 (e from -117 to
- * 120), and the padding columns must be zero. */
+ * x / 2^e to nearest even, where e = 120 to 240 at most (256 would stand for
+ * 2^128); infinities and NaN become NaN and do not affect the scale.  A power of
+ * two costs no precision, and every value is exact in bf16.  Scales made
+ * elsewhere must have bytes 10 to 247 (e from -117 to 120), e4m3 numbers beside
+ * the byte 247 must be at most 240, and the padding columns must be zero. */
 typedef struct {
   void* data;     /* device, muon_tensor8_bytes(rows, cols) bytes, 16-byte aligned */
   void* scale;    /* device, muon_tensor8_scale_bytes(...) bytes, 4-byte aligned */

@@ -26,15 +26,37 @@ __device__ __forceinline__ int scale_byte(unsigned u) {
   const int e = (int)(u >> 23) - 135 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
   return (e < -117 ? -117 : e) + 127;
 }
+// The byte of a block with a value above 1.75 * 2^127, the largest there is.
+constexpr int kTopScale = 247;
 // 2^e and 2^-e of a scale byte 10 .. 247: both normal fp32 numbers.
 __device__ __forceinline__ float scale_of(int byte) { return __uint_as_float((unsigned)byte << 23); }
 __device__ __forceinline__ float inv_scale_of(int byte) {
   return __uint_as_float((unsigned)(254 - byte) << 23);
 }
 
+// An infinity divided by a scale stays one: it is replaced by NaN before the
+// conversion, whose own result for it depends on the wave's overflow mode.
+__device__ __forceinline__ float inf_to_nan(float x) {
+  return (__float_as_uint(x) & 0x7fffffffu) == 0x7f800000u ? __uint_as_float(0x7fc00000u) : x;
+}
+// Eight values divided by their block's scale.  In a block of the largest scale,
+// 2^120, e4m3's 256 would stand for 2^128, which neither fp32 nor bf16 has: what
+// would round to it (248 * 2^120 and above, both types' largest among them) takes
+// 240, at most 2^-4 off, which is e4m3's half step too.
+__device__ __forceinline__ void to_units(const float (&v)[8], int byte, float (&w)[8]) {
+  const float inv = inv_scale_of(byte);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = inf_to_nan(v[i]) * inv;
+  if (byte == kTopScale) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)  // (a NaN stays)
+      w[i] = w[i] > 240.f ? 240.f : w[i] < -240.f ? -240.f : w[i];
+  }
+}
+
 // Eight values, already divided by their scale, as e4m3 bytes (rounded to
 // nearest even).  The scaled magnitudes are at most 448, so nothing
-// overflows; an infinity or NaN becomes e4m3's NaN.
+// overflows; a NaN becomes e4m3's NaN.
 __device__ __forceinline__ u32x2_t to_e4m3(const float (&v)[8]) {
   u32x2_t o;
 #pragma unroll
@@ -45,11 +67,6 @@ __device__ __forceinline__ u32x2_t to_e4m3(const float (&v)[8]) {
     o[w] = (unsigned)p;
   }
   return o;
-}
-// An infinity divided by a scale stays one: it is replaced by NaN before the
-// conversion, whose own result for it depends on the wave's overflow mode.
-__device__ __forceinline__ float inf_to_nan(float x) {
-  return (__float_as_uint(x) & 0x7fffffffu) == 0x7f800000u ? __uint_as_float(0x7fc00000u) : x;
 }
 
 __device__ __forceinline__ void from_e4m3(u32x2_t q, float scale, float (&v)[8]) {

@@ -115,9 +115,7 @@ __global__ __launch_bounds__(TEAM > 4 ? 64 * TEAM : 256) void layer_norm_kernel(
           top = top > f ? top : f;
         }
         const int byte = scale_byte(max16(top));
-        const float inv = inv_scale_of(byte);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = inf_to_nan(y[i]) * inv;
+        to_units(y, byte, y);
         if (col[k] < a.ld) *reinterpret_cast<u32x2_t*>(a.y8 + row * a.ld + col[k]) = to_e4m3(y);
         const unsigned word = pack_scales(byte);
         const int piece = k * TEAM + tw;

@@ -40,10 +40,8 @@ __global__ __launch_bounds__(256) void quantize8_rows_kernel(Quant8Args a, unsig
         top = top > f ? top : f;
       }
       const int byte = scale_byte(max16(top));
-      const float inv = inv_scale_of(byte);
       float w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = inf_to_nan(v[u][i]) * inv;
+      to_units(v[u], byte, w);
       if (c < a.ld) *reinterpret_cast<u32x2_t*>(a.q + (long long)row * a.ld + c) = to_e4m3(w);
       const unsigned word = pack_scales(byte);
       if (lane == 0)
@@ -87,13 +85,11 @@ __global__ __launch_bounds__(256) void quantize8_blocks_kernel(Quant8Args a, int
 #pragma unroll
   for (int w = 0; w < 4; ++w) top = top > tops[w] ? top : tops[w];
   const int byte = scale_byte(top);
-  const float inv = inv_scale_of(byte);
   unsigned q[8][2];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float w[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = inf_to_nan(v[i][j]) * inv;
+    to_units(v[i], byte, w);
     const u32x2_t o = to_e4m3(w);
     q[i][0] = o[0];
     q[i][1] = o[1];

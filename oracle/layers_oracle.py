@@ -42,10 +42,13 @@ def expand(e, shape, block_rows):
 
 
 def quantize8(x, block_rows):
-    """(e4m3 numbers, exponents) of a matrix."""
+    """(e4m3 numbers, exponents) of a matrix.  Where e = 120 numbers stop at
+    240: 256 * 2^120 is not a number of fp32 or bf16."""
     x = np.asarray(x, np.float64)
     e = block_exponents(x, block_rows)
-    return round_e4m3(x / expand(e, x.shape, block_rows)), e
+    scale = expand(e, x.shape, block_rows)
+    q = round_e4m3(x / scale)
+    return np.where(scale == 2.0 ** 120, np.clip(q, -240.0, 240.0), q), e
 
 
 def layer_norm(x, w, b, eps):

@@ -1,0 +1,23 @@
+"""Edges of the 8-bit linear layer and layer norm that need no GPU."""
+import numpy as np
+import pytest
+
+from oracle import layers_oracle as lo
+
+TOP = 2.0 ** 120
+BF16_MAX, FP32_MAX = 255 * TOP, (2 - 2.0 ** -23) * 2.0 ** 127
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+@pytest.mark.parametrize("v,q", [
+    (FP32_MAX, 240), (-FP32_MAX, -240), (BF16_MAX, 240), (-BF16_MAX, -240), (248 * TOP, 240),
+    (247.99 * TOP, 240), (240 * TOP, 240), (232 * TOP, 224), (232.01 * TOP, 240)])
+def test_oracle_largest_values_stay_finite(v, q, block_rows):
+    # a value of a block with e = 120 is within e4m3's half step, 2^-4 of it,
+    # and is a number of fp32 and bf16
+    x = np.array([[v, 1.0, FP32_MAX, np.inf, np.nan]])
+    got, e = lo.quantize8(x, block_rows)
+    assert e[0, 0] == 120 and got[0, 0] == q and got[0, 1] == 0 and np.isnan(got[0, 3:]).all()
+    value = got[0, 0] * TOP
+    assert np.isfinite(np.float32(value)) and abs(value) <= BF16_MAX
+    assert abs(value - v) <= 2.0 ** -4 * abs(v)

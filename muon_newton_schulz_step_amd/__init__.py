@@ -129,6 +129,17 @@ def _check_device(device, **tensors):
                 raise ValueError(f"{name}: every tensor must be on {device}, found {t.device}")
 
 
+def _workspace_tensor(workspace):
+    """A workspace that was given as a tensor, else None.  The library takes it as
+    one run of bytes from its first element on, so it has to be contiguous: the
+    gaps of a strided one, or what lies behind an expanded one, are not its own."""
+    if workspace is None or isinstance(workspace, Workspace):
+        return None
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace
+
+
 def _workspace(nbytes: int, device, workspace):
     if workspace is None:
         key = (str(device), _torch().cuda.current_stream(device).cuda_stream)
@@ -172,8 +183,7 @@ def orthogonalize(x, coeffs=QUINTIC, n_steps=None, *, eps=DEFAULT_EPS, compute="
     if n_steps is None and isinstance(coeffs[0], (int, float)):
         n_steps = 5
     table, n_steps = _coeffs(coeffs, n_steps)
-    _check_device(x.device, out=[out], workspace=[
-        workspace if workspace is not None and not isinstance(workspace, Workspace) else None])
+    _check_device(x.device, out=[out], workspace=[_workspace_tensor(workspace)])
     squeeze = x.dim() == 2
     xb = x.unsqueeze(0) if squeeze else x
     if xb.dim() != 3:
@@ -258,8 +268,7 @@ def _step(params, grads, bufs, second_moments, opt, *, mu, lr, scales, coeffs, n
     device = params[0].device
     _check_device(device, params=params, grads=grads, bufs=bufs,
                   second_moments=second_moments or [],
-                  workspace=[workspace if workspace is not None
-                             and not isinstance(workspace, Workspace) else None])
+                  workspace=[_workspace_tensor(workspace)])
     shapes = [tuple(p.shape) for p in params]
     rows = _lib.int_array(r for r, _ in shapes)
     cols = _lib.int_array(c for _, c in shapes)

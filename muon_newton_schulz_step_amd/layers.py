@@ -21,7 +21,7 @@ from __future__ import annotations
 import threading
 
 from . import _lib
-from . import MUON_BF16, MUON_FP32, MUON_OK, MuonError, Workspace, lib
+from . import MUON_BF16, MUON_FP32, MUON_OK, MuonError, Workspace, _workspace_tensor, lib
 
 _MAX_ROWS = _lib.MUON_MAX_ROWS
 
@@ -230,11 +230,6 @@ def _scratch(nbytes: int, index: int, workspace):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
-def _tensor_of(workspace):
-    """A workspace given as a tensor, for the device check."""
-    return None if workspace is None or isinstance(workspace, Workspace) else workspace
-
-
 def _call(index: int, name: str, *args):
     fn = _functions.get(name)
     if fn is None:
@@ -328,7 +323,7 @@ def weight_grad(dy, x, *, out_dtype=None, out=None, accumulate: bool = False, wo
     if out is not None and (out.shape != (n, k) or (out_dtype or out.dtype) != out.dtype
                             or not out.is_contiguous()):
         raise ValueError("out must be contiguous, (dy columns, x columns), and of out_dtype")
-    index = _device(dy, x, out, _tensor_of(workspace))
+    index = _device(dy, x, out, _workspace_tensor(workspace))
     if out is None:
         out = torch.empty(n, k, dtype=out_dtype or torch.float32, device=dy.device)
     _call_with_scratch(index, "muon_weight_grad", lib().muon_weight_grad_workspace_bytes(tokens, n, k),
@@ -390,7 +385,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, *, bias: bool = True, dweight
     mp, rp = _vector(mean, rows, "mean"), _vector(rstd, rows, "rstd")
     dwp = _vector(dweight, cols, "dweight") if dweight is not None else 0
     dbp = _vector(dbias, cols, "dbias") if dbias is not None else None
-    index = _device(dy, x, weight, mean, rstd, dweight, dbias, _tensor_of(workspace))
+    index = _device(dy, x, weight, mean, rstd, dweight, dbias, _workspace_tensor(workspace))
     device = dy.device
     dx = torch.empty(rows, cols, dtype=dy.dtype, device=device)
     if dweight is None:

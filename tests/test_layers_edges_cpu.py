@@ -1,7 +1,9 @@
 """Edges of the 8-bit linear layer and layer norm that need no GPU."""
 import numpy as np
 import pytest
+import torch
 
+import muon_newton_schulz_step_amd as mn
 from oracle import layers_oracle as lo
 
 TOP = 2.0 ** 120
@@ -21,3 +23,19 @@ def test_oracle_largest_values_stay_finite(v, q, block_rows):
     value = got[0, 0] * TOP
     assert np.isfinite(np.float32(value)) and abs(value) <= BF16_MAX
     assert abs(value - v) <= 2.0 ** -4 * abs(v)
+
+
+@pytest.mark.parametrize("workspace", [
+    torch.empty(1, dtype=torch.uint8).expand(1 << 30),              # 2^30 elements, one byte
+    torch.empty(1 << 12, dtype=torch.uint8)[::2], torch.empty(64, 64)[:, :32], torch.empty(64, 32).t()])
+def test_workspaces_with_gaps_are_refused(workspace):
+    # the library would write the gaps, or past the tensor's end
+    x, v, t = torch.zeros(4, 256), torch.zeros(256), mn.Tensor8.empty(4, 256)
+    one = [torch.zeros(8, 8)], [torch.zeros(8, 8)], [torch.zeros(8, 8)]
+    for bad in (lambda: mn.weight_grad(x.bfloat16(), t, workspace=workspace),
+                lambda: mn.layer_norm_backward(x, x, v, v[:4], v[:4], workspace=workspace),
+                lambda: mn.orthogonalize(x, workspace=workspace),
+                lambda: mn.step(*one, mu=0.9, lr=0.1, workspace=workspace),
+                lambda: mn.step_ex(*one, mu=0.9, lr=0.1, workspace=workspace)):
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            bad()

@@ -305,8 +305,14 @@ def matmul8(a, b, *, out_dtype=None, out=None):
     return out
 
 
+def _within_int(*sizes) -> bool:
+    """Whether the C ABI's ints can hold the sizes (ctypes cuts others off)."""
+    return all(-2 ** 31 <= v < 2 ** 31 for v in sizes)
+
+
 def weight_grad_workspace_bytes(tokens: int, n: int, k: int) -> int:
-    return int(lib().muon_weight_grad_workspace_bytes(tokens, n, k))
+    """Bytes of weight_grad's workspace; 0 also for sizes that it refuses."""
+    return int(lib().muon_weight_grad_workspace_bytes(tokens, n, k)) if _within_int(tokens, n, k) else 0
 
 
 def weight_grad(dy, x, *, out_dtype=None, out=None, accumulate: bool = False, workspace=None):
@@ -357,7 +363,8 @@ def layer_norm(x, weight, bias=None, *, eps: float = 1e-5, out_dtype=None):
 
 
 def layer_norm_backward_workspace_bytes(rows: int, cols: int) -> int:
-    return int(lib().muon_layer_norm_backward_workspace_bytes(rows, cols))
+    """Bytes of layer_norm_backward's workspace; 0 also for sizes that it refuses."""
+    return int(lib().muon_layer_norm_backward_workspace_bytes(rows, cols)) if _within_int(rows, cols) else 0
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, *, bias: bool = True, dweight=None,

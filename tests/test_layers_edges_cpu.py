@@ -39,3 +39,14 @@ def test_workspaces_with_gaps_are_refused(workspace):
                 lambda: mn.step_ex(*one, mu=0.9, lr=0.1, workspace=workspace)):
         with pytest.raises(ValueError, match="workspace must be contiguous"):
             bad()
+
+
+@pytest.mark.parametrize("past", [2 ** 31, 2 ** 32 + 16384, -2 ** 32 + 16384])
+def test_workspace_sizes_past_32_bits(past):
+    # 2^32 + 16384 tokens must not pass for 16384, which has partial sums
+    assert mn.weight_grad_workspace_bytes(16384, 48, 256) > 0
+    assert mn.layer_norm_backward_workspace_bytes(16384, 768) > 0
+    assert mn.weight_grad_workspace_bytes(past, 48, 256) == 0
+    assert mn.weight_grad_workspace_bytes(16384, 2 ** 32 + 48, 256) == 0
+    assert mn.layer_norm_backward_workspace_bytes(past, 768) == 0
+    assert mn.layer_norm_backward_workspace_bytes(16384, 2 ** 32 + 768) == 0

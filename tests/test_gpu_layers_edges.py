@@ -76,3 +76,47 @@ def test_products_of_the_largest_values(m, out):
     within(dw, d.T @ av, 2 * U * (m + 2) * (np.abs(d).T @ np.abs(av)) + 1e-300)
 
 
+@pytest.mark.parametrize("cols", [1, 3, 130, 768, 1283, 2048, 5120, 9000, 16384])
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_layer_norm_of_equal_values_gives_the_bias(cols, dtype):
+    # the mean of equal values is that value, whatever its last bits: the sum's
+    # rounding, d u of the value for d additions in a row (d < 64), is taken
+    # off again by the sum of the deviations, which leaves d^2 u^2, below half a step
+    announce("layer_norm of equal values", cols, dtype)
+    v = torch.cat([torch.tensor([1000.1, -0.1, 3.3e-5, 77777.77, 1 / 3], device=DEV),
+                   100 * randn(40, seed=cols)]).to(dtype)
+    x = v[:, None].expand(-1, cols).contiguous()
+    w, b = 1 + 0.3 * randn(cols, seed=2), 0.2 * randn(cols, seed=3)
+    y, mean, rstd = mn.layer_norm(x, w, b, eps=EPS, out_dtype=FP32)
+    assert torch.equal(mean, v.float())
+    assert torch.equal(y, b.expand(len(v), -1))
+    # no variance: the squares' mean and the correction's square are both below
+    # (64 u |v|)^2; one is off by d + 3 u of that, the other by 2 (d + 3) u
+    noise = 3 * 64 * U * (64 * U * np.abs(to64(v))) ** 2
+    within(rstd, np.full(len(v), EPS ** -0.5), EPS ** -0.5 * (noise / EPS + 4 * U))
+
+
+@pytest.mark.parametrize("cols", [768, 5120, 16384])
+def test_layer_norm_of_small_variance_around_a_large_mean(cols):
+    # the stored mean is the row's to half a step; y and rstd follow from it
+    announce("layer_norm around a large mean", cols)
+    x = 1000.1 + 1e-2 * randn(9, cols, seed=1)
+    w, b = 1 + 0.3 * randn(cols, seed=2), 0.2 * randn(cols, seed=3)
+    y, mean, rstd = mn.layer_norm(x, w, b, eps=EPS)
+    x64, w64, b64 = to64(x), to64(w), to64(b)
+    ry, rm, rr = lo.layer_norm(x64, w64, b64, EPS)
+    d = 32 + 6 + 16                                   # additions in a row
+    xc = np.abs(x64 - rm[:, None])
+    rough = (d + 1) * U * np.abs(x64).mean(1)         # the first mean's error
+    # the correction's error, and the rounding of the corrected mean
+    off = (d + 2) * U * (xc.mean(1) + rough) + U * (np.abs(rm) + rough)
+    within(mean, rm, off)
+    # the mean square of the deviations from the first mean, var + rough^2 at
+    # most, is off by d + 4 u; the square of the correction, which is taken off
+    # again, by 2 rough (d + 2) u (mean |xc| + rough) <= (d + 2) u (var + 3 rough^2)
+    var = (xc ** 2).mean(1)
+    rel = 0.5 * 2 * (d + 5) * U * (var + 2 * rough ** 2) / (var + EPS) + 4 * U
+    within(rstd, rr, rel * rr)
+    dev = off[:, None] + U * xc
+    by = np.abs(w64) * rr[:, None] * (dev + xc * (rel[:, None] + 4 * U)) + U * np.abs(ry)
+    within(y, ry, 1.001 * by)                         # (second order)

@@ -374,7 +374,9 @@ typedef struct {
                       and output of the launch read or written once */
   double exec_flops; /* flops the launch's MFMAs execute: its tiles over the
                         padded shape (lower-triangle tiles for GRAM, POLY and
-                        GRAMQ) */
+                        GRAMQ; MATMUL8 and WEIGHT_GRAD: whole tiles of their
+                        results, the summed axis in whole blocks of 128 and
+                        tiles of 64 tokens) */
 } muon_timing_record;
 
 /* Turn per-launch HIP-event timing on (1) or off (0) for later calls in

@@ -391,26 +391,38 @@ void tiles(Matmul8Args a, hipStream_t s) {
 }
 
 template <typename Y>
-void go(const Matmul8Args& a, hipStream_t s) {
+void go(const Matmul8Args& a, const Matmul8Plan& p, hipStream_t s) {
+  constexpr bool FP32 = std::is_same_v<Y, float>;
+  if (p.few) {
+    const dim3 grid((a.n + p.bn - 1) / p.bn), block(64 * kFewWaves);
+    if (p.bm == 16 && p.bn == 16)
+      hipLaunchKernelGGL((matmul8_rows_kernel<1, 1, Y>), grid, block, 0, s, a);
+    else if (p.bm == 16)
+      hipLaunchKernelGGL((matmul8_rows_kernel<1, 2, Y>), grid, block, 0, s, a);
+    else if (p.bn == 16)
+      hipLaunchKernelGGL((matmul8_rows_kernel<2, 1, Y>), grid, block, 0, s, a);
+    else
+      hipLaunchKernelGGL((matmul8_rows_kernel<2, 2, Y>), grid, block, 0, s, a);
+  } else if (p.bm == 64) {
+    tiles<64, 64, 2, 1, Y>(a, s);
+  } else if (p.bm == 128) {
+    tiles<128, 128, FP32 ? 4 : 2, 2, Y>(a, s);
+  } else {
+    tiles<256, 256, 4, 2, Y>(a, s);
+  }
+}
+}  // namespace
+
+Matmul8Plan matmul8_plan(int y_bf16, int m, int n, int ld) {
   // Few rows.  32 columns to a workgroup where that leaves 256 workgroups and
   // enough rows share the second half's saving (16 x 8192 x 4096: 11.1 -> 8.7 us,
   // 32 x 8192 x 4096: 16.6 -> 11.7 us; but 1 x 8192 x 8192: 13 -> 20 us, 16 x 8192
   // x 8192: 20 -> 22 us).  Past 16 rows a very wide product is faster in tiles (32
   // x 16384 x 4096: 22.8 -> 17.6 us).  A workgroup of 512 threads for 16 columns
   // reaches the 2^32 threads of a launch at 2^27 columns: tiles from there on.
-  if ((a.m <= 16 && a.n <= (1 << 26)) || (a.m <= 32 && a.n < 16384)) {
-    const dim3 block(64 * kFewWaves);
-    const bool two = a.n >= 8192 && (a.m > 16 || (a.m > 8 && a.ld <= 4096));
-    const dim3 grid(two ? (a.n + 31) / 32 : (a.n + 15) / 16);
-    if (a.m <= 16 && !two)
-      hipLaunchKernelGGL((matmul8_rows_kernel<1, 1, Y>), grid, block, 0, s, a);
-    else if (a.m <= 16)
-      hipLaunchKernelGGL((matmul8_rows_kernel<1, 2, Y>), grid, block, 0, s, a);
-    else if (!two)
-      hipLaunchKernelGGL((matmul8_rows_kernel<2, 1, Y>), grid, block, 0, s, a);
-    else
-      hipLaunchKernelGGL((matmul8_rows_kernel<2, 2, Y>), grid, block, 0, s, a);
-    return;
+  if ((m <= 16 && n <= (1 << 26)) || (m <= 32 && n < 16384)) {
+    const bool two = n >= 8192 && (m > 16 || (m > 8 && ld <= 4096));
+    return {true, m <= 16 ? 16 : 32, two ? 32 : 16};
   }
   // The tile by the time of the fullest CU, in us per k-tile.  Measured, for a
   // result in bf16: 256 x 256 (one per CU) 1.55; 128 x 128 0.72 alone and 0.88 for
@@ -424,29 +436,24 @@ void go(const Matmul8Args& a, hipStream_t s) {
   // columns and sums of 700 to 5120 the choice is on average within 0.3% of the
   // fastest of the three for either type (worst: 16384 x 5120 x 1280 in fp32,
   // whose stores bound it, 273 us against 232).
-  constexpr bool FP32 = std::is_same_v<Y, float>;
+  const bool fp32 = !y_bf16;
   auto share = [&](int bm, int bn) {  // tiles of the fullest CU
-    return (double)(((long long)((a.m + bm - 1) / bm) * ((a.n + bn - 1) / bn) + 255) / 256);
+    return (double)(((long long)((m + bm - 1) / bm) * ((n + bn - 1) / bn) + 255) / 256);
   };
   const double q256 = share(256, 256), q128 = share(128, 128), q64 = share(64, 64);
   const double odd = (long long)q128 % 2 ? 1.0 : 0.0;
-  const double t256 = (FP32 ? 3.3 : 1.55) * q256;
-  const double t128 = FP32 ? 0.9 * q128 + 0.2 * odd : 0.44 * q128 + 0.28 * odd;
-  const double t64 = FP32 ? 0.3 + 0.265 * q64 : 0.1 + 0.2 * q64;
-  if (t64 < t128 && t64 < t256)
-    tiles<64, 64, 2, 1, Y>(a, s);
-  else if (t128 < t256)
-    tiles<128, 128, FP32 ? 4 : 2, 2, Y>(a, s);
-  else
-    tiles<256, 256, 4, 2, Y>(a, s);
+  const double t256 = (fp32 ? 3.3 : 1.55) * q256;
+  const double t128 = fp32 ? 0.9 * q128 + 0.2 * odd : 0.44 * q128 + 0.28 * odd;
+  const double t64 = fp32 ? 0.3 + 0.265 * q64 : 0.1 + 0.2 * q64;
+  const int b = t64 < t128 && t64 < t256 ? 64 : t128 < t256 ? 128 : 256;
+  return {false, b, b};
 }
-}  // namespace
 
-hipError_t launch_matmul8(int y_bf16, const Matmul8Args& a, hipStream_t s) {
+hipError_t launch_matmul8(int y_bf16, const Matmul8Args& a, const Matmul8Plan& p, hipStream_t s) {
   if (y_bf16)
-    go<bf16_t>(a, s);
+    go<bf16_t>(a, p, s);
   else
-    go<float>(a, s);
+    go<float>(a, p, s);
   return hipGetLastError();
 }
 

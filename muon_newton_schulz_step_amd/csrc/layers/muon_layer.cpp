@@ -71,6 +71,8 @@ bool pieces_fit(int rows, int cols) {
 bool tiles_fit(long long rows, long long cols) {
   return (double)((rows + 63) / 64) * (double)((cols + 63) / 64) < 2147483648.0;
 }
+// A size in whole tiles, for the flops that a launch executes.
+double padded(long long size, int tile) { return (double)((size + tile - 1) / tile * tile); }
 int status_of(hipError_t e) { return e == hipSuccess ? MUON_OK : MUON_ERR_HIP; }
 
 size_t norm_workspace(int rows, int cols) {
@@ -164,10 +166,13 @@ int muon_matmul8(const muon_tensor8* a, const muon_tensor8* b, void* y, int y_dt
   g.ld = (int)ld8(a->cols); g.sld = (int)scale_ld8(a->cols);
   g.shift_a = shift_of(a); g.shift_b = shift_of(b);
   g.y = y; g.ldy = ldy;
+  const Matmul8Plan plan = matmul8_plan(y_dtype == MUON_BF16, g.m, g.n, g.ld);
   const double m = g.m, n = g.n, k = a->cols;
-  return status_of(timed_launch(MUON_K_MATMUL8, g.m, g.n, 2 * m * n * k, 2 * m * n * g.ld,
-                                m * k + n * k + m * n * size_of(y_dtype), stream,
-                                [&] { return launch_matmul8(y_dtype == MUON_BF16, g, stream); }));
+  return status_of(timed_launch(
+      MUON_K_MATMUL8, g.m, g.n, 2 * m * n * k,
+      2 * padded(g.m, plan.bm) * padded(g.n, plan.bn) * g.ld,
+      m * k + n * k + m * n * size_of(y_dtype), stream,
+      [&] { return launch_matmul8(y_dtype == MUON_BF16, g, plan, stream); }));
 }
 
 size_t muon_weight_grad_workspace_bytes(int tokens, int n, int k) {
@@ -212,7 +217,8 @@ int muon_weight_grad(const void* dy, int dy_dtype, long long lddy, int tokens, i
   g.part = need ? static_cast<float*>(workspace) : nullptr;
   const double t = tokens, k = x->cols;
   return status_of(timed_launch(
-      MUON_K_WEIGHT_GRAD, n, x->cols, 2 * t * n * k, 2 * t * n * k,
+      MUON_K_WEIGHT_GRAD, n, x->cols, 2 * t * n * k,
+      2 * padded(tokens, kTileT) * padded(n, plan.bn) * padded(x->cols, plan.bk),
       2 * t * n + t * k + n * k * size_of(dw_dtype) * (accumulate ? 2 : 1), stream,
       [&] { return launch_weight_grad(dw_dtype == MUON_BF16, g, plan, stream); }));
 }

@@ -57,9 +57,16 @@ struct Matmul8Args {
   long long ldy;
   int tiles_m, tiles_n, group_m;
 };
-hipError_t launch_matmul8(int y_bf16, const Matmul8Args& a, hipStream_t s);
+// The kernel of a product and the bm x bn results of y that a workgroup computes.
+struct Matmul8Plan {
+  bool few;  // the kernel for few rows
+  int bm, bn;
+};
+Matmul8Plan matmul8_plan(int y_bf16, int m, int n, int ld);
+hipError_t launch_matmul8(int y_bf16, const Matmul8Args& a, const Matmul8Plan& p, hipStream_t s);
 
-// dw[n][k] (+)= sum_t dy[t][n] x[t][k]
+// dw[n][k] (+)= sum_t dy[t][n] x[t][k], in tiles of kTileT tokens
+constexpr int kTileT = 64;
 struct WeightGradArgs {
   const void* dy;           // bf16
   long long lddy;

@@ -18,7 +18,6 @@
 
 namespace muon {
 
-constexpr int kTileT = 64;  // tokens per LDS tile
 constexpr int kGroupN = 4;
 
 // Wait until this wave has no LDS operation in flight (lgkmcnt(0), the other

@@ -120,3 +120,21 @@ def test_layer_norm_of_small_variance_around_a_large_mean(cols):
     dev = off[:, None] + U * xc
     by = np.abs(w64) * rr[:, None] * (dev + xc * (rel[:, None] + 4 * U)) + U * np.abs(ry)
     within(y, ry, 1.001 * by)                         # (second order)
+
+
+def test_executed_flops_count_whole_tiles():
+    announce("executed flops of the layers' launches")
+    a, b = mn.quantize8(randn(517, 300, seed=1)), mn.quantize8(randn(771, 300, seed=2))
+    mn.timing_read()
+    mn.timing_enable(True)
+    try:
+        mn.matmul8(mn.quantize8(randn(5, 300, seed=3)), b)          # 16 x 16 to a workgroup
+        mn.matmul8(a, b)                                            # 64 x 64
+        mn.weight_grad(randn(517, 130, seed=4, dtype=BF16), a)      # 64 tokens, 128 x 128
+        torch.cuda.synchronize()
+    finally:
+        mn.timing_enable(False)
+    recs = [r for r in mn.timing_read() if r["kind"] in ("matmul8", "weight_grad")]
+    assert [r["flops"] for r in recs] == [2.0 * 5 * 771 * 300, 2.0 * 517 * 771 * 300, 2.0 * 517 * 130 * 300]
+    assert [r["exec_flops"] for r in recs] == [2.0 * 16 * 784 * 384, 2.0 * 576 * 832 * 384,
+                                               2.0 * 576 * 256 * 384]

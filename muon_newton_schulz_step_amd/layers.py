@@ -15,6 +15,8 @@ step of its weights:
     step([W], [dW], [buf], mu=0.95, lr=0.02)
 
 The backward passes are calls of their own: autograd records none of these.
+Matrices may have a row stride, and begin at a multiple of 16 bytes (every new
+tensor does; a slice that does not is refused: clone() it first).
 """
 from __future__ import annotations
 

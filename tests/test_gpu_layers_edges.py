@@ -138,3 +138,33 @@ def test_executed_flops_count_whole_tiles():
     assert [r["flops"] for r in recs] == [2.0 * 5 * 771 * 300, 2.0 * 517 * 771 * 300, 2.0 * 517 * 130 * 300]
     assert [r["exec_flops"] for r in recs] == [2.0 * 16 * 784 * 384, 2.0 * 576 * 832 * 384,
                                                2.0 * 576 * 256 * 384]
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_one_row_of_a_larger_tensor(dtype):
+    # a row that begins at a multiple of 16 bytes is taken where it lies, any
+    # other one refused
+    announce("one row of a larger tensor", dtype)
+    whole = randn(131, 389, seed=4, dtype=dtype)
+    row, other = whole[8:9], whole[5:6]
+    assert row.data_ptr() % 16 == 0 and other.data_ptr() % 16 != 0
+    w, b = 1 + 0.3 * randn(389, seed=2), 0.2 * randn(389, seed=3)
+    own = row.clone()
+    for block_rows in (1, 128):
+        check8(mn.quantize8(row, block_rows), row, block_rows)
+    t, tt = mn.quantize8(row, 128, transposed=True)
+    check8(tt, row.t(), 128)
+    y, mean, rstd = mn.layer_norm(row, w, b)
+    assert all(torch.equal(p, q) for p, q in zip((y, mean, rstd), mn.layer_norm(own, w, b)))
+    assert all(torch.equal(p, q) for p, q in zip(mn.layer_norm_backward(row, row, w, mean, rstd),
+                                                 mn.layer_norm_backward(own, own, w, mean, rstd)))
+    calls = [lambda x: mn.quantize8(x), lambda x: mn.quantize8(x, 128), lambda x: mn.layer_norm(x, w, b),
+             lambda x: mn.layer_norm_backward(x, own, w, mean, rstd),
+             lambda x: mn.layer_norm_backward(own, x, w, mean, rstd)]
+    if dtype == BF16:
+        assert torch.equal(mn.weight_grad(row, t), mn.weight_grad(own, t))
+        calls.append(lambda x: mn.weight_grad(x, t))
+    for call in calls:
+        with pytest.raises(mn.MuonError) as err:
+            call(other)
+        assert err.value.status == mn.MUON_ERR_INVALID_ARG

@@ -296,7 +296,11 @@ int muon_dequantize8(const muon_tensor8* t, void* y, int y_dtype, long long ldy,
  * fp32.  Either operand may have either kind of block.  For a bf16 result of
  * many rows the matrix instruction cuts each product off 13 bits below the
  * largest of its group of 8 along k (about 1.5e-5 of the result's norm, far
- * below the rounding to bf16); fp32 results come from exact products. */
+ * below the rounding to bf16); fp32 results, and those of few rows (up to 16,
+ * and up to 32 where b has less than 16384), come from exact products.  The
+ * order of the sums depends on the sizes too, so a row may come out different in
+ * its last bits with another number of rows beside it; the same call always
+ * gives the same result. */
 int muon_matmul8(const muon_tensor8* a, const muon_tensor8* b, void* y, int y_dtype,
                  long long ldy, hipStream_t stream);
 
@@ -319,7 +323,8 @@ int muon_weight_grad(const void* dy, int dy_dtype, long long lddy, int tokens, i
  * weight, bias: fp32, cols elements; bias NULL: zero.  The output goes to y
  * (bf16 or fp32) or, with y NULL, to the 8-bit tensor y8 (rows x cols,
  * block_rows 1), rounded once from fp32; exactly one of the two is given.
- * mean, rstd: fp32, rows elements, written for the backward pass. */
+ * mean, rstd: fp32, rows elements, written for the backward pass.  All of it is
+ * computed in fp32: a row whose sums or squares overflow it gives what they give. */
 int muon_layer_norm(const void* x, int x_dtype, long long ldx, int rows, int cols,
                     const float* weight, const float* bias, float eps, void* y, int y_dtype,
                     long long ldy, const muon_tensor8* y8, float* mean, float* rstd,

@@ -6,9 +6,11 @@
 //             dw = sum over rows of dy xh, db = sum over rows of dy
 // All sums are fp32.  Both passes read each row once and are bound by HBM.
 //
-//   16384 x 1280 fp32 to bf16 23.7 us (5.3 TB/s), 8192 x 4096 bf16 24.4 us
+//   16384 x 1280 fp32 to bf16 23.8 us (5.3 TB/s), 8192 x 4096 bf16 24.4 us
 //   (5.5 TB/s); backward 8192 x 4096 bf16 39.8 us (5.1 TB/s) and 4.3 us for the
-//   reduction of 256 partial sums.  A 1 GiB copy runs at 5.2.
+//   reduction of 256 partial sums.  A 1 GiB copy runs at 5.2.  Short of that:
+//   to 8 bits 16384 x 1280 21 us (3.0 TB/s), backward 4099 x 1280 from 8 bits
+//   12.5 + 3.1 us (two rows to a wave, a join and a second launch).
 // While a row is worked on, the team's next one is on its way (without: 30 us
 // forward and 64 us backward of 8192 x 4096).
 //
@@ -339,9 +341,14 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* part, in
 namespace {
 // Team and chunks for a row of `cols` columns.  Forward: one wave up to 2048,
 // four up to 8192, eight up to 16384; the fewest chunks that hold the row.
-// Backward: at most three chunks to a lane, where the team can be larger
-// instead, since four with their gradient sums spill in fp32 (16000 x 8192 fp32,
-// four waves of four chunks: 720 us; eight of two: 198 us).
+// Backward: up to 8192 columns at most three chunks to a lane, with a larger
+// team where that takes one, since four fill the registers with their gradient
+// sums: 16000 x 8192, eight waves of two chunks against four of four, 292 and 316
+// us with dy and x in fp32, 238 and 264 (x bf16), 215 and 239 (x 8 bits), 190 and
+// 204 (dy bf16, x fp32); with dy in bf16 and x in bf16 or 8 bits the eight cost
+// more, 156 and 153, 139 and 129.  12289 to 16384 columns take four chunks on
+// eight waves and spill 1 to 10 registers, 54 with dy and x in fp32 (16000 x
+// 16384: 285 us all bf16, 602 all fp32).
 template <bool BACK, typename F>
 void with_shape(int cols, F&& f) {
 #define MUON_SHAPE(T, N) f(std::integral_constant<int, T>{}, std::integral_constant<int, N>{})

@@ -55,7 +55,8 @@ __device__ __forceinline__ i32x8_t frag8(const u32x4_t& lo, const u32x4_t& hi) {
 // MFMAs cover the other's waits (16384 x 16384 x 4096: 874 -> 822 us).
 //   256 x 256 tiles on 8 waves, inputs in the caches: 8192 x 4096 x 4096 103 to
 //   110 us by box (2.5 to 2.67 PFLOP/s), 16384 x 16384 x 4096 788 to 798 us (2.75
-//   to 2.80), to fp32 216 and 1766 us (1.25).
+//   to 2.80), to fp32 216 and 1766 us (1.25).  They take all 256 registers and
+//   spill 8 (28 bytes a lane; to fp32 2).
 //   A library's product with one scale per tensor runs at 2.72 to 2.80.  At the
 //   larger size the MFMAs are busy 70% of the cycles and the chip runs at 1.68
 //   GHz: it is bound by power.  Without the stores of y it would take 752 us.
@@ -435,7 +436,10 @@ Matmul8Plan matmul8_plan(int y_bf16, int m, int n, int ld) {
   // 1280: 31.6, 13.7, 12.7 us.)  Over 64 sizes of 48 to 16384 rows, 700 to 16384
   // columns and sums of 700 to 5120 the choice is on average within 0.3% of the
   // fastest of the three for either type (worst: 16384 x 5120 x 1280 in fp32,
-  // whose stores bound it, 273 us against 232).
+  // whose stores bound it, 273 us against 232).  A fourth tile of 64 x 128, not
+  // here, was faster at some middle sizes: in bf16 by up to 9% (1024 x 4096 x 4096:
+  // 25.8 -> 23.7 us), in fp32 by up to 18% (1024 x 1280 x 5120: 31.1 -> 26.3 us); over
+  // the 64 sizes the choice is 0.8% and 2.7% off the fastest of all four.
   const bool fp32 = !y_bf16;
   auto share = [&](int bm, int bn) {  // tiles of the fullest CU
     return (double)(((long long)((m + bm - 1) / bm) * ((n + bn - 1) / bn) + 255) / 256);

@@ -347,6 +347,38 @@ int muon_layer_norm_backward(const void* dy, int dy_dtype, long long lddy, const
                              float* dbias, int accumulate, void* workspace,
                              size_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------ gradient clipping */
+
+/* In front of the step: the norm of all gradients together, and their
+ * clipping to it.
+ *   norm = sqrt(sum over all tensors of g^2)
+ *   g    <- c g,  c = max_norm / (norm + eps) where that is below 1, else 1
+ *   n           number of tensors, up to 2^20; 0: the norm is 0.
+ *   sizes       host array of n element counts, 0 to 2^38 each.
+ *   grads       host array of n device pointers (NULL where a size is 0),
+ *               aligned to their element type.
+ *   dtypes      host array of n element types.
+ *   out         NULL: in place; or host array of n device pointers for the
+ *               clipped tensors, of the types out_dtypes.  out[i] may be
+ *               grads[i] where the types are the same too.
+ *   max_norm    finite, >= 0;  eps: finite, >= 0.
+ *   norm        device, one fp32 number.
+ *   workspace   muon_grad_norm_workspace_bytes, possibly 0 (then it may be
+ *               NULL), MUON_WORKSPACE_ALIGN-aligned.
+ * Squares and sums are fp64, so no finite gradient overflows them; c has
+ * fp32's precision, and a clipped value is rounded once from c g in fp32.  With an infinite norm c
+ * is 0 (an infinite gradient becomes NaN), with a NaN it is a NaN, and so is
+ * every gradient: a caller that would rather skip such a step reads the norm.
+ * In place, gradients that are not clipped are not written.  Written ranges
+ * must overlap no other range (MUON_ERR_INVALID_ARG); the same gradient may
+ * stand in the list twice only where it is not written. */
+size_t muon_grad_norm_workspace_bytes(int n, const long long* sizes);
+int muon_grad_norm(int n, const long long* sizes, const void* const* grads, const int* dtypes,
+                   float* norm, void* workspace, size_t workspace_bytes, hipStream_t stream);
+int muon_clip_grads(int n, const long long* sizes, const void* const* grads, const int* dtypes,
+                    void* const* out, const int* out_dtypes, float max_norm, float eps,
+                    float* norm, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* ------------------------------------------------------------ measurement */
 
 /* Kernel classes reported by the timing log. */
@@ -364,7 +396,8 @@ typedef enum {
   MUON_K_MATMUL8 = 10,
   MUON_K_WEIGHT_GRAD = 11,
   MUON_K_LAYER_NORM = 12,     /* forward */
-  MUON_K_LAYER_NORM_BACK = 13 /* backward, with the reduction of its sums */
+  MUON_K_LAYER_NORM_BACK = 13, /* backward, with the reduction of its sums */
+  MUON_K_GRAD_NORM = 14        /* the gradients' norm, and their clipping: all of a call's launches */
 } muon_kernel_kind;
 
 typedef struct {

@@ -17,6 +17,10 @@ and, for the linear layers those matrices belong to (``layers.py``):
     weight_grad(dy, x8)                            dy^T x from the 8-bit activation
     layer_norm(x, weight, bias)                    y, mean, rstd
     layer_norm_backward(dy, x, weight, mean, rstd) dx, dweight, dbias
+
+and in front of the step (``clipping.py``):
+
+    grad_norm(grads), clip_grads(grads, max_norm)  the norm of all gradients together
 """
 from __future__ import annotations
 
@@ -381,3 +385,4 @@ from .layers import (  # noqa: E402,F401
     Tensor8, dequantize8, layer_norm, layer_norm_backward, layer_norm_backward_workspace_bytes,
     matmul8, quantize8, weight_grad, weight_grad_workspace_bytes,
 )
+from .clipping import clip_grads, grad_norm  # noqa: E402,F401

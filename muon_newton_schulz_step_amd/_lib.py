@@ -17,7 +17,8 @@ MUON_MAX_COLS8 = 1 << 22
 MUON_MAX_ROWS = 2 ** 31 - 256
 MUON_MAX_NORM_COLS = 16384
 KERNEL_KINDS = ("prep", "norm", "gram", "poly", "update", "final", "normuon", "apply",
-                "gramq", "quant8", "matmul8", "weight_grad", "layer_norm", "layer_norm_back")
+                "gramq", "quant8", "matmul8", "weight_grad", "layer_norm", "layer_norm_back",
+                "grad_norm")
 
 # Every symbol include/muon.h declares.
 EXPORTS = (
@@ -44,6 +45,9 @@ EXPORTS = (
     "muon_layer_norm",
     "muon_layer_norm_backward_workspace_bytes",
     "muon_layer_norm_backward",
+    "muon_grad_norm_workspace_bytes",
+    "muon_grad_norm",
+    "muon_clip_grads",
 )
 
 
@@ -130,6 +134,7 @@ def load() -> ctypes.CDLL:
     lib.muon_timing_read.argtypes = [ctypes.POINTER(MuonTimingRecord), ctypes.c_int, _c_int_p]
     lib.muon_timing_read.restype = ctypes.c_int
     i, ll, sz, t8 = ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t, ctypes.POINTER(MuonTensor8)
+    f = ctypes.c_float
     for name, restype, argtypes in (
             ("muon_tensor8_bytes", sz, [i, i]),
             ("muon_tensor8_scale_bytes", sz, [i, i, i]),
@@ -142,7 +147,10 @@ def load() -> ctypes.CDLL:
                                     _vp, _vp, _vp]),
             ("muon_layer_norm_backward_workspace_bytes", sz, [i, i]),
             ("muon_layer_norm_backward", i, [_vp, i, ll, _vp, i, ll, t8, i, i, _vp, _vp, _vp, _vp,
-                                             ll, _vp, _vp, i, _vp, sz, _vp])):
+                                             ll, _vp, _vp, i, _vp, sz, _vp]),
+            ("muon_grad_norm_workspace_bytes", sz, [i, _vp]),
+            ("muon_grad_norm", i, [i, _vp, _vp, _vp, _vp, _vp, sz, _vp]),
+            ("muon_clip_grads", i, [i, _vp, _vp, _vp, _vp, _vp, f, f, _vp, _vp, sz, _vp])):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = restype, argtypes
     _lib = lib

@@ -304,6 +304,47 @@ int muon_dequantize8(const muon_tensor8* t, void* y, int y_dtype, long long ldy,
 int muon_matmul8(const muon_tensor8* a, const muon_tensor8* b, void* y, int y_dtype,
                  long long ldy, hipStream_t stream);
 
+/* Activations of a linear layer.  GELU is z Phi(z) with the normal distribution
+ * function (within 0.75e-7 of it), GELU_TANH its tanh form; RELU2 is
+ * max(z, 0)^2.  RELU's slope at 0 is 0. */
+typedef enum {
+  MUON_ACT_NONE = 0,
+  MUON_ACT_RELU = 1,
+  MUON_ACT_RELU2 = 2,
+  MUON_ACT_GELU = 3,
+  MUON_ACT_GELU_TANH = 4,
+  MUON_ACT_SILU = 5
+} muon_activation;
+
+/* The product with all that follows it in a block, in its epilogue:
+ *   z = a b^T + bias,  y = act(z) + residual
+ * in fp32 up to the one rounding of each output.
+ *   bias        fp32, one per row of b; NULL: none.
+ *   residual    m x n, bf16 or fp32; NULL: none.
+ *   z           m x n, kept for the backward pass, of y's type, bf16 beside an
+ *               8-bit result; NULL: not kept.
+ *   y or y8     exactly one: bf16 or fp32, or (y NULL) an 8-bit tensor with
+ *               1-row blocks, the operand of the next product.
+ * Sums are those of muon_matmul8; an 8-bit result's are those of a bf16 one of
+ * more than 32 rows, and exact up to 32. */
+int muon_linear8(const muon_tensor8* a, const muon_tensor8* b, const float* bias, int activation,
+                 const void* residual, int residual_dtype, long long ldr, void* z, long long ldz,
+                 void* y, int y_dtype, long long ldy, const muon_tensor8* y8, hipStream_t stream);
+
+/* Its backward pass up to the two gradient products: dz = dy act'(z), and
+ *   dz    bf16, weight_grad's operand; NULL: not written
+ *   dz8   8-bit, 1-row blocks, the operand of dx = dz W; NULL: not written
+ *   dbias fp32, cols elements, the sum of dz over the rows, added to with
+ *         accumulate; NULL: not computed
+ * each rounded once from fp32; at least one is given.  z (bf16 or fp32) is what
+ * muon_linear8 kept; with MUON_ACT_NONE it is not read and may be NULL.  The
+ * residual's gradient is dy itself.  The workspace is needed for dbias alone. */
+size_t muon_linear8_backward_workspace_bytes(int rows, int cols);
+int muon_linear8_backward(const void* dy, int dy_dtype, long long lddy, const void* z, int z_dtype,
+                          long long ldz, int activation, int rows, int cols, void* dz,
+                          long long lddz, const muon_tensor8* dz8, float* dbias, int accumulate,
+                          void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* dw = dy^T x, or with accumulate dw += dy^T x: the gradient of W (n x k,
  * dense, as muon_step takes it) from the layer's output gradient dy (tokens x
  * n, bf16, lddy <= 2^26; fp32 and longer strides return MUON_ERR_UNSUPPORTED)
@@ -397,7 +438,9 @@ typedef enum {
   MUON_K_WEIGHT_GRAD = 11,
   MUON_K_LAYER_NORM = 12,     /* forward */
   MUON_K_LAYER_NORM_BACK = 13, /* backward, with the reduction of its sums */
-  MUON_K_GRAD_NORM = 14        /* the gradients' norm, and their clipping: all of a call's launches */
+  MUON_K_GRAD_NORM = 14,       /* the gradients' norm, and their clipping: all of a call's launches */
+  MUON_K_LINEAR8 = 15,
+  MUON_K_LINEAR8_BACK = 16
 } muon_kernel_kind;
 
 typedef struct {
@@ -412,7 +455,7 @@ typedef struct {
                       and output of the launch read or written once */
   double exec_flops; /* flops the launch's MFMAs execute: its tiles over the
                         padded shape (lower-triangle tiles for GRAM, POLY and
-                        GRAMQ; MATMUL8 and WEIGHT_GRAD: whole tiles of their
+                        GRAMQ; MATMUL8, LINEAR8 and WEIGHT_GRAD: whole tiles of their
                         results, the summed axis in whole blocks of 128 and
                         tiles of 64 tokens) */
 } muon_timing_record;

@@ -14,6 +14,8 @@ and, for the linear layers those matrices belong to (``layers.py``):
 
     quantize8(x), dequantize8(t)                   8-bit tensors (Tensor8)
     matmul8(a, b)                                  a b^T of two 8-bit tensors
+    linear8(a, b, bias, activation=, residual=)    act(a b^T + bias) + residual
+    linear8_backward(dy, z, activation=)           dz, dz in 8 bits, dbias
     weight_grad(dy, x8)                            dy^T x from the 8-bit activation
     layer_norm(x, weight, bias)                    y, mean, rstd
     layer_norm_backward(dy, x, weight, mean, rstd) dx, dweight, dbias
@@ -383,6 +385,7 @@ def timing_read(cap: int = 1 << 16):
 
 from .layers import (  # noqa: E402,F401
     Tensor8, dequantize8, layer_norm, layer_norm_backward, layer_norm_backward_workspace_bytes,
-    matmul8, quantize8, weight_grad, weight_grad_workspace_bytes,
+    linear8, linear8_backward, linear8_backward_workspace_bytes, matmul8, quantize8, weight_grad,
+    weight_grad_workspace_bytes,
 )
 from .clipping import clip_grads, grad_norm  # noqa: E402,F401

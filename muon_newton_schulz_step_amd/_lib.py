@@ -8,6 +8,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmuon.so")
 
 MUON_BF16, MUON_FP32 = 0, 1
+ACTIVATIONS = {None: 0, "relu": 1, "relu2": 2, "gelu": 3, "gelu_tanh": 4, "silu": 5}
 MUON_OK, MUON_ERR_INVALID_ARG, MUON_ERR_UNSUPPORTED, MUON_ERR_WORKSPACE, MUON_ERR_HIP = 0, -1, -2, -3, -4
 MUON_MAX_STEPS = 64
 MUON_WORKSPACE_ALIGN = 256
@@ -18,7 +19,7 @@ MUON_MAX_ROWS = 2 ** 31 - 256
 MUON_MAX_NORM_COLS = 16384
 KERNEL_KINDS = ("prep", "norm", "gram", "poly", "update", "final", "normuon", "apply",
                 "gramq", "quant8", "matmul8", "weight_grad", "layer_norm", "layer_norm_back",
-                "grad_norm")
+                "grad_norm", "linear8", "linear8_back")
 
 # Every symbol include/muon.h declares.
 EXPORTS = (
@@ -45,6 +46,9 @@ EXPORTS = (
     "muon_layer_norm",
     "muon_layer_norm_backward_workspace_bytes",
     "muon_layer_norm_backward",
+    "muon_linear8",
+    "muon_linear8_backward_workspace_bytes",
+    "muon_linear8_backward",
     "muon_grad_norm_workspace_bytes",
     "muon_grad_norm",
     "muon_clip_grads",
@@ -148,6 +152,10 @@ def load() -> ctypes.CDLL:
             ("muon_layer_norm_backward_workspace_bytes", sz, [i, i]),
             ("muon_layer_norm_backward", i, [_vp, i, ll, _vp, i, ll, t8, i, i, _vp, _vp, _vp, _vp,
                                              ll, _vp, _vp, i, _vp, sz, _vp]),
+            ("muon_linear8", i, [t8, t8, _vp, i, _vp, i, ll, _vp, ll, _vp, i, ll, t8, _vp]),
+            ("muon_linear8_backward_workspace_bytes", sz, [i, i]),
+            ("muon_linear8_backward", i, [_vp, i, ll, _vp, i, ll, i, i, i, _vp, ll, t8, _vp, i, _vp,
+                                          sz, _vp]),
             ("muon_grad_norm_workspace_bytes", sz, [i, _vp]),
             ("muon_grad_norm", i, [i, _vp, _vp, _vp, _vp, _vp, sz, _vp]),
             ("muon_clip_grads", i, [i, _vp, _vp, _vp, _vp, _vp, f, f, _vp, _vp, sz, _vp])):

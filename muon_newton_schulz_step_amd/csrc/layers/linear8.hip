@@ -1,0 +1,78 @@
+// linear8: the product with an epilogue, its choice of a kernel and a tile, and
+// its launch (the kernels: matmul8_kernels.h).
+#include "matmul8_kernels.h"
+
+namespace muon {
+
+namespace {
+constexpr int kOut8 = 2;
+
+template <int BM, int BN, int WGM, int WGN, typename Y>
+void tiles(Linear8Args a, hipStream_t s) {
+  constexpr bool EXACT = std::is_same_v<Y, float>;
+  a.tiles_m = (a.m + BM - 1) / BM;
+  a.tiles_n = (a.n + BN - 1) / BN;
+  a.group_m = 6;  // as for the plain product
+  const dim3 grid((unsigned)a.tiles_m * (unsigned)a.tiles_n), block(64 * WGM * WGN);
+  // results larger than the last-level cache are stored past it, as there
+  const double bytes = (double)a.m * a.n * (sizeof(Y) + (a.z ? sizeof(KeptOf<Y>) : 0));
+  if (bytes > 256.0 * (1 << 20))
+    hipLaunchKernelGGL((matmul8_tile_kernel<BM, BN, WGM, WGN, EXACT, true, Y, true>), grid, block, 0, s, a);
+  else
+    hipLaunchKernelGGL((matmul8_tile_kernel<BM, BN, WGM, WGN, EXACT, false, Y, true>), grid, block, 0, s, a);
+}
+
+template <typename Y>
+void go(const Linear8Args& a, const Matmul8Plan& p, hipStream_t s) {
+  constexpr bool FP32 = std::is_same_v<Y, float>;
+  if (p.few) {
+    const dim3 grid((a.n + p.bn - 1) / p.bn), block(64 * kFewWaves);
+    if constexpr (is8<Y>) {
+      if (p.bm == 16)
+        hipLaunchKernelGGL((matmul8_rows_kernel<1, 8, Y, true>), grid, block, 0, s, a);
+      else
+        hipLaunchKernelGGL((matmul8_rows_kernel<2, 8, Y, true>), grid, block, 0, s, a);
+    } else {
+      if (p.bm == 16 && p.bn == 16)
+        hipLaunchKernelGGL((matmul8_rows_kernel<1, 1, Y, true>), grid, block, 0, s, a);
+      else if (p.bm == 16)
+        hipLaunchKernelGGL((matmul8_rows_kernel<1, 2, Y, true>), grid, block, 0, s, a);
+      else if (p.bn == 16)
+        hipLaunchKernelGGL((matmul8_rows_kernel<2, 1, Y, true>), grid, block, 0, s, a);
+      else
+        hipLaunchKernelGGL((matmul8_rows_kernel<2, 2, Y, true>), grid, block, 0, s, a);
+    }
+  } else if (p.bm == 64) {
+    if constexpr (!is8<Y>) tiles<64, 64, 2, 1, Y>(a, s);
+  } else if (p.bm == 128) {
+    tiles<128, 128, FP32 ? 4 : 2, 2, Y>(a, s);
+  } else {
+    tiles<256, 256, 4, 2, Y>(a, s);
+  }
+}
+}  // namespace
+
+Matmul8Plan linear8_plan(int out, int m, int n, int ld) {
+  if (out != kOut8) return matmul8_plan(out == MUON_BF16, m, n, ld);
+  // An 8-bit result needs whole blocks of 128 columns in a workgroup.
+  if (m <= 32) return {true, m <= 16 ? 16 : 32, 128};
+  // the costs of the plain product's tiles
+  auto share = [&](int b) {
+    return (double)(((long long)((m + b - 1) / b) * ((n + b - 1) / b) + 255) / 256);
+  };
+  const double q128 = share(128), odd = (long long)q128 % 2 ? 1.0 : 0.0;
+  const int b = 0.44 * q128 + 0.28 * odd < 1.55 * share(256) ? 128 : 256;
+  return {false, b, b};
+}
+
+hipError_t launch_linear8(int out, const Linear8Args& a, const Matmul8Plan& p, hipStream_t s) {
+  if (out == kOut8)
+    go<unsigned char>(a, p, s);
+  else if (out == MUON_BF16)
+    go<bf16_t>(a, p, s);
+  else
+    go<float>(a, p, s);
+  return hipGetLastError();
+}
+
+}  // namespace muon

@@ -312,6 +312,108 @@ def matmul8(a, b, *, out_dtype=None, out=None):
     return out
 
 
+def _activation(name) -> int:
+    code = _lib.ACTIVATIONS.get(name)
+    if code is None:
+        raise ValueError(f"unknown activation {name!r} (None, "
+                         f"{', '.join(repr(a) for a in _lib.ACTIVATIONS if a)})")
+    return code
+
+
+def linear8(a, b, bias=None, *, activation=None, residual=None, keep: bool = False,
+            out_dtype=None, out=None):
+    """act(a b^T + bias) + residual of two Tensor8, (m, k) and (n, k) -> (m, n) in
+    bf16 (default), fp32, or torch.float8_e4m3fn: a Tensor8 with blocks of
+    1 x 128, the next product's operand.  ``bias`` is fp32, ``residual`` bf16 or fp32;
+    ``activation`` None, "relu", "relu2" (squared), "gelu", "gelu_tanh" or
+    "silu".  ``keep`` returns (y, z) with z = a b^T + bias for linear8_backward, in
+    y's dtype (bf16 beside a Tensor8).  ``out`` (bf16 or fp32) may have a row stride.
+    Everything is fp32 up to the one rounding of each result; the sums are those
+    of matmul8."""
+    torch = _T or _torch()
+    if a.cols != b.cols:
+        raise ValueError(f"a and b must have the same number of columns: {a.cols}, {b.cols}")
+    act = _activation(activation)
+    if keep and not act:
+        raise ValueError("keep is for an activation: without one the backward pass needs no z")
+    m, n = a.rows, b.rows
+    bp = _vector(bias, n, "bias") if bias is not None else None
+    index = _device(a, b, bias, residual, out)
+    device = a.device
+    rp, rcode, ldr = None, MUON_BF16, n
+    if residual is not None:
+        if residual.shape != (m, n):
+            raise ValueError("residual must be (a.rows, b.rows)")
+        rcode = _dtype_code(residual.dtype)
+        if n:
+            rp, _, _, ldr = _matrix(residual, "residual")
+    out8 = out is None and out_dtype == torch.float8_e4m3fn
+    if out8 and n == 0:
+        raise ValueError("an 8-bit result has at least one column")
+    if out8:
+        out = Tensor8.empty(m, n, 1, device)
+        yp, code, ldy, y8 = None, MUON_BF16, n, out._c
+    elif out is None:
+        out = torch.empty(m, n, dtype=out_dtype or torch.bfloat16, device=device)
+        yp, code, ldy, y8 = out.data_ptr(), _dtype_code(out.dtype), max(n, 1), None
+    else:
+        if out.shape != (m, n) or (out_dtype or out.dtype) != out.dtype:
+            raise ValueError("out must be (a.rows, b.rows) and of out_dtype")
+        yp, _, _, ldy = _matrix(out, "out") if n else (0, m, n, 1)
+        code, y8 = _dtype_code(out.dtype), None
+    z = zp = None
+    if keep:
+        z = torch.empty(m, n, dtype=torch.bfloat16 if out8 else out.dtype, device=device)
+        zp = z.data_ptr()
+    _call(index, "muon_linear8", a._c, b._c, bp, act, rp, rcode, ldr, zp, n, yp, code, ldy, y8)
+    return (out, z) if keep else out
+
+
+def linear8_backward_workspace_bytes(rows: int, cols: int) -> int:
+    """Bytes of linear8_backward's workspace; 0 also for sizes that it refuses."""
+    return int(lib().muon_linear8_backward_workspace_bytes(rows, cols)) if _within_int(rows, cols) else 0
+
+
+def linear8_backward(dy, z=None, *, activation=None, bias: bool = True, dbias=None,
+                     accumulate: bool = False, workspace=None):
+    """(dz, dz8, dbias) of linear8 from its output gradient ``dy`` (rows, n), bf16 or
+    fp32: dz = dy act'(z) in bf16 for weight_grad and as a Tensor8 for the input's
+    gradient, matmul8(dz8, w8t), and its sum over the rows.  ``z`` is what linear8
+    kept; without an activation it is not needed, and a bf16 ``dy`` is itself dz.
+    ``dbias`` (fp32) may be given, and is added to with ``accumulate``; ``bias``
+    False: no dbias (None).  The residual's gradient is dy."""
+    torch = _T or _torch()
+    act = _activation(activation)
+    dyp, rows, cols, lddy = _matrix(dy, "dy")
+    dcode = _dtype_code(dy.dtype)
+    zp, zcode, ldz = None, MUON_BF16, cols
+    if act:
+        if z is None or z.shape != dy.shape:
+            raise ValueError("an activation needs z, of dy's shape")
+        zp, _, _, ldz = _matrix(z, "z")
+        zcode = _dtype_code(z.dtype)
+    if not bias and dbias is not None:
+        raise ValueError("dbias was given with bias=False")
+    if accumulate and dbias is None:
+        raise ValueError("accumulate needs dbias")
+    dbp = _vector(dbias, cols, "dbias") if dbias is not None else None
+    index = _device(dy, z if act else None, dbias, _workspace_tensor(workspace))
+    device = dy.device
+    dz8 = Tensor8.empty(rows, cols, 1, device)
+    if act or dcode != MUON_BF16:
+        dz = torch.empty(rows, cols, dtype=torch.bfloat16, device=device)
+        dzp = dz.data_ptr()
+    else:
+        dz, dzp = dy, None
+    if bias and dbias is None:
+        dbias = torch.empty(cols, dtype=torch.float32, device=device)
+        dbp = dbias.data_ptr()
+    need = lib().muon_linear8_backward_workspace_bytes(rows, cols) if bias else 0
+    _call_with_scratch(index, "muon_linear8_backward", need, workspace, dyp, dcode, lddy, zp, zcode,
+                       ldz, act, rows, cols, dzp, cols, dz8._c, dbp, 1 if accumulate else 0)
+    return dz, dz8, dbias
+
+
 def _within_int(*sizes) -> bool:
     """Whether the C ABI's ints can hold the sizes (ctypes cuts others off)."""
     return all(-2 ** 31 <= v < 2 ** 31 for v in sizes)

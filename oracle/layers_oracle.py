@@ -3,6 +3,7 @@ infrastructure; shares no code with the GPU path)."""
 from __future__ import annotations
 
 import numpy as np
+from scipy.special import expit, ndtr
 
 MIN_EXP = -117
 
@@ -66,3 +67,43 @@ def layer_norm_backward(dy, x, w, mean, rstd):
     dx = np.asarray(rstd, np.float64)[:, None] * (
         g - g.mean(1, keepdims=True) - xh * (g * xh).mean(1, keepdims=True))
     return dx, (dy * xh).sum(0), dy.sum(0)
+
+
+ACTIVATIONS = (None, "relu", "relu2", "gelu", "gelu_tanh", "silu")
+_TANH = 2.0 * np.sqrt(2.0 / np.pi)  # (1 + tanh u) / 2 = 1 / (1 + exp(-2 u))
+
+
+def activation(z, act):
+    z = np.asarray(z, np.float64)
+    if act is None:
+        return z
+    if act == "relu":
+        return np.maximum(z, 0.0)
+    if act == "relu2":
+        return np.maximum(z, 0.0) ** 2
+    if act == "gelu":
+        return z * ndtr(z)
+    return z * expit(_TANH * (z + 0.044715 * z ** 3) if act == "gelu_tanh" else z)
+
+
+def activation_grad(z, act):
+    """The activation's slope; relu's is 0 at 0."""
+    z = np.asarray(z, np.float64)
+    if act is None:
+        return np.ones_like(z)
+    if act == "relu":
+        return (z > 0).astype(np.float64)
+    if act == "relu2":
+        return 2.0 * np.maximum(z, 0.0)
+    if act == "gelu":
+        return ndtr(z) + z * np.exp(-z * z / 2) / np.sqrt(2 * np.pi)
+    u, du = (_TANH * (z + 0.044715 * z ** 3), _TANH * (1 + 3 * 0.044715 * z * z)) \
+        if act == "gelu_tanh" else (z, 1.0)
+    return expit(u) + z * expit(u) * expit(-u) * du
+
+
+def linear8(av, bv, bias, act, residual):
+    """(y, z) of the values of two 8-bit tensors."""
+    z = av @ bv.T + (0.0 if bias is None else np.asarray(bias, np.float64))
+    y = activation(z, act)
+    return (y if residual is None else y + np.asarray(residual, np.float64)), z

@@ -388,6 +388,84 @@ int muon_layer_norm_backward(const void* dy, int dy_dtype, long long lddy, const
                              float* dbias, int accumulate, void* workspace,
                              size_t workspace_bytes, hipStream_t stream);
 
+/* The norms after and before a block, fused with the block's gate and the
+ * residual stream's scale:
+ *   p = N(branch) * post_weight + post_bias   (post_weight NULL: the branch itself)
+ *   r = scale * x + gate * p
+ *   h = N(r) * weight + bias
+ * N is layer norm, or with `rms` RMS norm, both with eps in the square root:
+ * (v - mean) * rstd, rstd = 1 / sqrt(sum((v - mean)^2) / cols + eps), with a mean of 0
+ * for RMS.  Vectors are fp32 of cols elements, scale one fp32 number on the
+ * device; all but weight may be NULL (post_bias only with post_weight): bias and
+ * post_bias 0, gate and scale 1. */
+typedef struct {
+  const float* weight;
+  const float* bias;
+  const float* post_weight;
+  const float* post_bias;
+  const float* gate;
+  const float* scale;
+  float eps; /* finite, >= 0 */
+  int rms;   /* 0 or 1 */
+} muon_residual_params;
+
+/*   x, r        rows x cols (cols up to MUON_MAX_NORM_COLS, more returns
+ *               MUON_ERR_UNSUPPORTED), both of x_dtype, the residual stream before
+ *               and after.  r NULL: not written, which needs branch and scale
+ *               NULL (r is x then).
+ *   branch      bf16, or fp32 beside an fp32 x (a bf16 x with an fp32 branch
+ *               returns MUON_ERR_UNSUPPORTED); NULL: none, r = scale * x, which
+ *               needs post_weight and gate NULL.
+ *   h or h8     exactly one: bf16 or fp32, or (h NULL) an 8-bit tensor with
+ *               1-row blocks.
+ *   stats       fp32, 4 x rows, for the backward pass: mean and rstd of r, mean
+ *               and rstd of the branch (0 without its norm).
+ * All of it is fp32 up to the one rounding of each output: h and stats come
+ * from r before it is rounded to x's type. */
+int muon_residual_norm(const void* x, int x_dtype, long long ldx, const void* branch,
+                       int branch_dtype, long long ldb, int rows, int cols,
+                       const muon_residual_params* params, void* r, long long ldr, void* h,
+                       int h_dtype, long long ldh, const muon_tensor8* h8, float* stats,
+                       hipStream_t stream);
+
+/* The gradients of its parameters, fp32; NULL: not computed. */
+typedef struct {
+  float* weight;
+  float* bias;
+  float* post_weight;
+  float* post_bias;
+  float* gate;
+  float* scale;
+} muon_residual_grads;
+
+/* Its backward pass, from the gradients dr of r (x_dtype; NULL: none) and dh of h
+ * (branch_dtype, whatever h's type was).  With rh = (r - mean) * rstd, bh likewise
+ * (the branch itself without its norm), g = dh * weight and sums over a row's
+ * columns (RMS: without the terms sum(g) and sum(e)):
+ *   d = dr + rstd * (g - sum(g) / cols - rh * sum(g rh) / cols)
+ *   dx = scale * d                              (x_dtype)
+ *   e = d * gate * post_weight
+ *   dbranch = rstd' * (e - sum(e) / cols - bh * sum(e bh) / cols), or e without the
+ *             branch's norm                     (branch_dtype; NULL: not written)
+ * and over the rows: weight sum(dh rh), bias sum(dh), post_weight gate * sum(d bh),
+ * post_bias gate * sum(d), gate sum(d p), scale sum over all of d x.
+ *   r, stats    the forward pass's (its x where it wrote no r).
+ *   branch      as there; read only where params has post_weight or gate, may be
+ *               NULL otherwise.
+ *   x           as there; read only for the scale's gradient, may be NULL otherwise.
+ *   grads       those of parameters that params does not have must be NULL;
+ *               added to with accumulate.
+ *   workspace   muon_residual_norm_backward_workspace_bytes for these sizes
+ *               (`branch_params` 1 where params has post_weight or gate, else 0). */
+size_t muon_residual_norm_backward_workspace_bytes(int rows, int cols, int branch_params);
+int muon_residual_norm_backward(const void* dr, long long lddr, const void* dh, long long lddh,
+                                const void* r, long long ldr, const void* branch, long long ldb,
+                                const void* x, long long ldx, int x_dtype, int branch_dtype,
+                                int rows, int cols, const muon_residual_params* params,
+                                const float* stats, void* dx, long long lddx, void* dbranch,
+                                long long lddb, const muon_residual_grads* grads, int accumulate,
+                                void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* ------------------------------------------------------ gradient clipping */
 
 /* In front of the step: the norm of all gradients together, and their
@@ -440,7 +518,9 @@ typedef enum {
   MUON_K_LAYER_NORM_BACK = 13, /* backward, with the reduction of its sums */
   MUON_K_GRAD_NORM = 14,       /* the gradients' norm, and their clipping: all of a call's launches */
   MUON_K_LINEAR8 = 15,
-  MUON_K_LINEAR8_BACK = 16
+  MUON_K_LINEAR8_BACK = 16,
+  MUON_K_RESIDUAL_NORM = 17,
+  MUON_K_RESIDUAL_NORM_BACK = 18 /* with the reduction of its sums */
 } muon_kernel_kind;
 
 typedef struct {

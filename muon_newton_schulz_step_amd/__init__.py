@@ -20,6 +20,11 @@ and, for the linear layers those matrices belong to (``layers.py``):
     layer_norm(x, weight, bias)                    y, mean, rstd
     layer_norm_backward(dy, x, weight, mean, rstd) dx, dweight, dbias
 
+between a block and the next one (``block.py``):
+
+    residual_norm(x, branch, weight, bias, ...)    r, h, stats: residual sum and norms
+    residual_norm_backward(dr, dh, r, branch, ...) dx, dbranch and the parameters' gradients
+
 and in front of the step (``clipping.py``):
 
     grad_norm(grads), clip_grads(grads, max_norm)  the norm of all gradients together
@@ -387,5 +392,8 @@ from .layers import (  # noqa: E402,F401
     Tensor8, dequantize8, layer_norm, layer_norm_backward, layer_norm_backward_workspace_bytes,
     linear8, linear8_backward, linear8_backward_workspace_bytes, matmul8, quantize8, weight_grad,
     weight_grad_workspace_bytes,
+)
+from .block import (  # noqa: E402,F401
+    ResidualNormGrads, residual_norm, residual_norm_backward, residual_norm_backward_workspace_bytes,
 )
 from .clipping import clip_grads, grad_norm  # noqa: E402,F401

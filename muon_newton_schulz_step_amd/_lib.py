@@ -19,7 +19,8 @@ MUON_MAX_ROWS = 2 ** 31 - 256
 MUON_MAX_NORM_COLS = 16384
 KERNEL_KINDS = ("prep", "norm", "gram", "poly", "update", "final", "normuon", "apply",
                 "gramq", "quant8", "matmul8", "weight_grad", "layer_norm", "layer_norm_back",
-                "grad_norm", "linear8", "linear8_back")
+                "grad_norm", "linear8", "linear8_back",
+                "residual_norm", "residual_norm_back")
 
 # Every symbol include/muon.h declares.
 EXPORTS = (
@@ -49,6 +50,9 @@ EXPORTS = (
     "muon_linear8",
     "muon_linear8_backward_workspace_bytes",
     "muon_linear8_backward",
+    "muon_residual_norm",
+    "muon_residual_norm_backward_workspace_bytes",
+    "muon_residual_norm_backward",
     "muon_grad_norm_workspace_bytes",
     "muon_grad_norm",
     "muon_clip_grads",
@@ -75,6 +79,17 @@ class MuonTimingRecord(ctypes.Structure):
 class MuonTensor8(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p),
                 ("rows", ctypes.c_int), ("cols", ctypes.c_int), ("block_rows", ctypes.c_int)]
+
+
+class MuonResidualParams(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in (
+        "weight", "bias", "post_weight", "post_bias", "gate", "scale")] + [
+            ("eps", ctypes.c_float), ("rms", ctypes.c_int)]
+
+
+class MuonResidualGrads(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in (
+        "weight", "bias", "post_weight", "post_bias", "gate", "scale")]
 
 
 _c_int_p = ctypes.POINTER(ctypes.c_int)
@@ -138,7 +153,7 @@ def load() -> ctypes.CDLL:
     lib.muon_timing_read.argtypes = [ctypes.POINTER(MuonTimingRecord), ctypes.c_int, _c_int_p]
     lib.muon_timing_read.restype = ctypes.c_int
     i, ll, sz, t8 = ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t, ctypes.POINTER(MuonTensor8)
-    f = ctypes.c_float
+    f, rp, rg = ctypes.c_float, ctypes.POINTER(MuonResidualParams), ctypes.POINTER(MuonResidualGrads)
     for name, restype, argtypes in (
             ("muon_tensor8_bytes", sz, [i, i]),
             ("muon_tensor8_scale_bytes", sz, [i, i, i]),
@@ -156,6 +171,11 @@ def load() -> ctypes.CDLL:
             ("muon_linear8_backward_workspace_bytes", sz, [i, i]),
             ("muon_linear8_backward", i, [_vp, i, ll, _vp, i, ll, i, i, i, _vp, ll, t8, _vp, i, _vp,
                                           sz, _vp]),
+            ("muon_residual_norm", i, [_vp, i, ll, _vp, i, ll, i, i, rp, _vp, ll, _vp, i, ll, t8,
+                                       _vp, _vp]),
+            ("muon_residual_norm_backward_workspace_bytes", sz, [i, i, i]),
+            ("muon_residual_norm_backward", i, [_vp, ll, _vp, ll, _vp, ll, _vp, ll, _vp, ll, i, i, i,
+                                                i, rp, _vp, _vp, ll, _vp, ll, rg, i, _vp, sz, _vp]),
             ("muon_grad_norm_workspace_bytes", sz, [i, _vp]),
             ("muon_grad_norm", i, [i, _vp, _vp, _vp, _vp, _vp, sz, _vp]),
             ("muon_clip_grads", i, [i, _vp, _vp, _vp, _vp, _vp, f, f, _vp, _vp, sz, _vp])):

@@ -24,7 +24,7 @@ SOURCES = ["gemm_update.hip", "gemm_final_w.hip", "gemm_final_out.hip", "gemm_gr
            "gemm_poly.hip", "gemm_fp32.hip", "muon_kernels.hip", "muon_peaks.hip",
            "muon_static.hip", "layers/quantize8.hip", "layers/layer_norm.hip",
            "layers/matmul8.hip", "layers/weight_grad.hip",
-           "layers/linear8.hip", "layers/linear8_backward.hip",
+           "layers/linear8.hip", "layers/linear8_backward.hip", "layers/residual_norm.hip",
            "grad_norm.hip", "muon_api.cpp", "layers/muon_layer.cpp", "layers/muon_block.cpp",
            "muon_clip.cpp"]
 ARCH = os.environ.get("MUON_OFFLOAD_ARCH", "gfx950")

@@ -107,3 +107,61 @@ def linear8(av, bv, bias, act, residual):
     z = av @ bv.T + (0.0 if bias is None else np.asarray(bias, np.float64))
     y = activation(z, act)
     return (y if residual is None else y + np.asarray(residual, np.float64)), z
+
+
+def _norm(v, rms, eps):
+    """(v - mean) rstd, mean, rstd of each row; a mean of 0 for RMS norm."""
+    mean = np.zeros(v.shape[0]) if rms else v.mean(1)
+    c = v - mean[:, None]
+    rstd = 1.0 / np.sqrt((c * c).mean(1) + eps)
+    return c * rstd[:, None], mean, rstd
+
+
+def _or(v, otherwise):
+    return otherwise if v is None else np.asarray(v, np.float64)
+
+
+def residual_norm(x, branch, w, b=None, pw=None, pb=None, gate=None, scale=None, rms=False,
+                  eps=1e-5):
+    """(r, h, stats of 4 x rows)."""
+    x = np.asarray(x, np.float64)
+    pmean = prstd = np.zeros(x.shape[0])
+    p = 0.0
+    if branch is not None:
+        p = np.asarray(branch, np.float64)
+        if pw is not None:
+            p, pmean, prstd = _norm(p, rms, eps)
+            p = p * pw + _or(pb, 0.0)
+    r = _or(scale, 1.0) * x + _or(gate, 1.0) * p
+    rh, mean, rstd = _norm(r, rms, eps)
+    return r, rh * w + _or(b, 0.0), np.stack((mean, rstd, pmean, prstd))
+
+
+def residual_norm_backward(dr, dh, r, branch, w, stats, x=None, pw=None, pb=None, gate=None,
+                           scale=None, rms=False):
+    """Gradients by name, with the forward pass's statistics."""
+    dh, r = np.asarray(dh, np.float64), np.asarray(r, np.float64)
+    st = np.asarray(stats, np.float64)[:, :, None]
+
+    def back(g, vh, rstd):
+        out = g - vh * (g * vh).mean(1, keepdims=True)
+        return rstd * (out if rms else out - g.mean(1, keepdims=True))
+
+    rh = (r - st[0]) * st[1]
+    d = _or(dr, 0.0) + back(dh * w, rh, st[1])
+    out = dict(dx=_or(scale, 1.0) * d, dweight=(dh * rh).sum(0), dbias=dh.sum(0))
+    if scale is not None:
+        out["dscale"] = (d * np.asarray(x, np.float64)).sum()
+    if branch is None:
+        return out
+    bh = np.asarray(branch, np.float64)
+    if pw is not None:
+        bh = (bh - st[2]) * st[3]
+    g = _or(gate, 1.0)
+    out["dgate"] = (d * (bh * _or(pw, 1.0) + _or(pb, 0.0))).sum(0)
+    if pw is None:
+        out["dbranch"] = d * g + np.zeros_like(bh)
+    else:
+        out["dpost_weight"], out["dpost_bias"] = (g * d * bh).sum(0), (g * d).sum(0)
+        out["dbranch"] = back(d * g * pw, bh, st[3])
+    return out

@@ -15,21 +15,24 @@ __device__ __forceinline__ float sigmoid(float u) {
   return rcp_fast(1.f + exp2_fast(-1.44269504f * u));
 }
 
-// The normal distribution function, and with it exp(-z^2 / 2): Abramowitz and
-// Stegun 7.1.26, erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + p x) with
-// x = |z| / sqrt(2), within 1.5e-7, so within 0.75e-7 of the function; a tenth of
-// the instructions of the library's erfc, which an epilogue of 268 million values
-// would wait for (0.4 ms beside a product of 0.8 ms).
-__device__ __forceinline__ float normal_cdf(float z, float& density) {
-  const float x = 0.70710678f * fabsf(z);
-  const float t = rcp_fast(fmaf(0.3275911f, x, 1.f));
-  float p = fmaf(1.061405429f, t, -1.453152027f);
-  p = fmaf(p, t, 1.421413741f);
-  p = fmaf(p, t, -0.284496736f);
-  p = fmaf(p, t, 0.254829592f);
-  density = exp2_fast(-1.44269504f * (x * x));
-  const float half = 0.5f * (p * t) * density;
-  return z > 0.f ? 1.f - half : half;
+// The normal distribution's tail beyond |z|, Phi(-|z|), and exp(-z^2 / 2): Abramowitz
+// and Stegun 7.1.26, erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + p x) with
+// x = |z| / sqrt(2), within 1.5e-7, here halved; a tenth of the instructions of the
+// library's erfc, which an epilogue of 268 million values would wait for (0.4 ms
+// beside a product of 0.8 ms).
+__device__ __forceinline__ float normal_tail(float z, float& density) {
+  const float t = rcp_fast(fmaf(0.23164190f, fabsf(z), 1.f));  // p / sqrt(2)
+  float p = fmaf(0.5307027145f, t, -0.7265760135f);
+  p = fmaf(p, t, 0.7107068705f);
+  p = fmaf(p, t, -0.142248368f);
+  p = fmaf(p, t, 0.127414796f);
+  density = exp2_fast(-0.72134752f * (z * z));
+  return p * t * density;
+}
+// z Phi(z): for z > 0 z - z tail, else z tail
+__device__ __forceinline__ float gelu(float z) {
+  float e;
+  return fmaf(-fabsf(z), normal_tail(z, e), __builtin_fmaxf(z, 0.f));
 }
 
 // (a NaN is below nothing and stays one)
@@ -40,26 +43,22 @@ __device__ __forceinline__ float tanh_arg(float z) {
   return z * fmaf(0.071354816f, z * z, 1.5957691f);
 }
 
-// `act` is the same for all lanes: one branch for eight values.
-__device__ __forceinline__ void activate(float (&v)[8], int act) {
-  if (act == MUON_ACT_RELU || act == MUON_ACT_RELU2) {
+// `act` is the same for all lanes: one branch for all of the values.
+template <int S, int N>
+__device__ __forceinline__ void activate(float (&v)[S][N], int act) {
+  auto each = [&](auto&& f) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = relu(v[i]);
-    if (act == MUON_ACT_RELU2)
+    for (int s = 0; s < S; ++s)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= v[i];
-  } else if (act == MUON_ACT_GELU) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float e;
-      v[i] *= normal_cdf(v[i], e);
-    }
-  } else if (act == MUON_ACT_GELU_TANH) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= sigmoid(tanh_arg(v[i]));
-  } else if (act == MUON_ACT_SILU) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= sigmoid(v[i]);
+      for (int i = 0; i < N; ++i) v[s][i] = f(v[s][i]);
+  };
+  switch (act) {
+    case MUON_ACT_RELU: each([](float z) { return relu(z); }); break;
+    case MUON_ACT_RELU2: each([](float z) { return relu(z) * relu(z); }); break;
+    case MUON_ACT_GELU: each([](float z) { return gelu(z); }); break;
+    case MUON_ACT_GELU_TANH: each([](float z) { return z * sigmoid(tanh_arg(z)); }); break;
+    case MUON_ACT_SILU: each([](float z) { return z * sigmoid(z); }); break;
+    default: break;
   }
 }
 
@@ -76,7 +75,8 @@ __device__ __forceinline__ void activate_grad(float (&d)[8], const float (&z)[8]
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float e;
-      const float c = normal_cdf(z[i], e);
+      const float tail = normal_tail(z[i], e);
+      const float c = z[i] > 0.f ? 1.f - tail : tail;
       d[i] *= fmaf(0.39894228f * z[i], e, c);
     }
   } else if (act == MUON_ACT_GELU_TANH) {

@@ -236,6 +236,34 @@ struct Raw8<float> {
   }
 };
 
+// Eight values of a block that 16 lanes of a DPP row hold, divided by the block's
+// scale: w and the scale's byte, as scale_byte(max16(finite_bits)) and to_units give
+// them, for a quarter of their instructions.  The largest magnitude is taken as
+// floats (a NaN is no number's maximum); only where it is an infinity, a NaN or in
+// reach of the largest scale does the block go the long way.
+__device__ __forceinline__ int block_units(const float (&v)[8], float (&w)[8]) {
+  float t = __builtin_fmaxf(fabsf(v[0]), fabsf(v[1]));
+#pragma unroll
+  for (int i = 2; i < 8; ++i) t = __builtin_fmaxf(t, fabsf(v[i]));
+  unsigned top = max16(__float_as_uint(t));
+  if (__builtin_expect(top > 0x7f600000u, 0)) {  // 448 * 2^119
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const unsigned f = finite_bits(v[i]);
+      top = top > f ? top : f;
+    }
+    const int byte = scale_byte(max16(top));
+    to_units(v, byte, w);
+    return byte;
+  }
+  const int byte = scale_byte(top);
+  const float inv = inv_scale_of(byte);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = v[i] * inv;
+  return byte;
+}
+
 // The four scale bytes of a wave whose rows of 16 lanes each hold one, as a
 // word (the same in all lanes).
 __device__ __forceinline__ unsigned pack_scales(int byte) {

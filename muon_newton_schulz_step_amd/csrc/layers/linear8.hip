@@ -7,9 +7,14 @@ namespace muon {
 namespace {
 constexpr int kOut8 = 2;
 
-template <int BM, int BN, int WGM, int WGN, typename Y>
+// Whether an 8-bit result comes from exact products.  Rounding to 8 bits turns an
+// error of relative size e into flips of a whole step for a share e / 2^-4 of the
+// values, sqrt(e 2^-4) in the norm.  The 8-bit instruction's cut leaves e near
+// 1e-4 where a few columns of a are 64 times the others.  XXX
+bool exact8(int m, int ld) { return ld <= 512 || m <= 512; }
+
+template <int BM, int BN, int WGM, int WGN, bool EXACT, typename Y>
 void tiles(Linear8Args a, hipStream_t s) {
-  constexpr bool EXACT = std::is_same_v<Y, float>;
   a.tiles_m = (a.m + BM - 1) / BM;
   a.tiles_n = (a.n + BN - 1) / BN;
   a.group_m = 6;  // as for the plain product
@@ -43,11 +48,18 @@ void go(const Linear8Args& a, const Matmul8Plan& p, hipStream_t s) {
         hipLaunchKernelGGL((matmul8_rows_kernel<2, 2, Y, true>), grid, block, 0, s, a);
     }
   } else if (p.bm == 64) {
-    if constexpr (!is8<Y>) tiles<64, 64, 2, 1, Y>(a, s);
+    if constexpr (!is8<Y>) tiles<64, 64, 2, 1, FP32, Y>(a, s);
+  } else if (is8<Y> && exact8(a.m, a.ld)) {
+    if constexpr (is8<Y>) {
+      if (p.bm == 128)
+        tiles<128, 128, 4, 2, true, Y>(a, s);
+      else
+        tiles<256, 256, 4, 2, true, Y>(a, s);
+    }
   } else if (p.bm == 128) {
-    tiles<128, 128, FP32 ? 4 : 2, 2, Y>(a, s);
+    tiles<128, 128, FP32 ? 4 : 2, 2, FP32, Y>(a, s);
   } else {
-    tiles<256, 256, 4, 2, Y>(a, s);
+    tiles<256, 256, 4, 2, FP32, Y>(a, s);
   }
 }
 }  // namespace
@@ -60,8 +72,10 @@ Matmul8Plan linear8_plan(int out, int m, int n, int ld) {
   auto share = [&](int b) {
     return (double)(((long long)((m + b - 1) / b) * ((n + b - 1) / b) + 255) / 256);
   };
-  const double q128 = share(128), odd = (long long)q128 % 2 ? 1.0 : 0.0;
-  const int b = 0.44 * q128 + 0.28 * odd < 1.55 * share(256) ? 128 : 256;
+  const double q128 = share(128), q256 = share(256), odd = (long long)q128 % 2 ? 1.0 : 0.0;
+  const bool small = exact8(m, ld) ? 0.9 * q128 + 0.2 * odd < 3.3 * q256
+                                : 0.44 * q128 + 0.28 * odd < 1.55 * q256;
+  const int b = small ? 128 : 256;
   return {false, b, b};
 }
 

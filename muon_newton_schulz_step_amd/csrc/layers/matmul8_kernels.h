@@ -41,48 +41,6 @@ template <typename Y> using KeptOf = std::conditional_t<std::is_same_v<Y, float>
 template <bool EPI> using ProductArgs = std::conditional_t<EPI, Linear8Args, Matmul8Args>;
 template <typename Y> constexpr bool is8 = std::is_same_v<Y, unsigned char>;
 
-// Eight columns of the epilogue in fp32, from the sums v of row m < g.m to what
-// is rounded: nothing on the way is, but for the z that is kept.
-template <bool STRM, typename Y>
-__device__ __forceinline__ void epilogue8(const Linear8Args& g, int m, int n, const float (&bias)[8],
-                                          float (&v)[8]) {
-#pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] += bias[e];
-  if (g.z)
-    store8_edge<STRM>(static_cast<KeptOf<Y>*>(g.z) + (long long)m * g.ldz + n, g.n - n, v);
-  activate(v, g.act);
-  if (g.res) {
-    float r[8];
-    const long long at = (long long)m * g.ldr + n;
-    if (g.res_fp32)
-      load8_edge(static_cast<const float*>(g.res) + at, g.n - n, r);
-    else
-      load8_edge(static_cast<const bf16_t*>(g.res) + at, g.n - n, r);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += r[e];
-  }
-}
-// The same for four columns; any of them may lie past the last one.
-template <typename Y>
-__device__ __forceinline__ void epilogue4(const Linear8Args& g, int m, int n, f32x4_t& s) {
-  float v[8] = {s[0], s[1], s[2], s[3], 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (g.bias && n + e < g.n) v[e] += g.bias[n + e];
-    if (g.z && n + e < g.n)
-      static_cast<KeptOf<Y>*>(g.z)[(long long)m * g.ldz + n + e] = from_f32<KeptOf<Y>>(v[e]);
-  }
-  activate(v, g.act);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (g.res && n + e < g.n) {
-      const long long at = (long long)m * g.ldr + n + e;
-      v[e] += g.res_fp32 ? static_cast<const float*>(g.res)[at]
-                         : to_f32(static_cast<const bf16_t*>(g.res)[at]);
-    }
-    s[e] = v[e];
-  }
-}
 // The scale byte of row m's block `b`; the last block's writer fills the row of
 // scales up, as blocks of zeros, so that equal tensors are equal byte by byte.
 __device__ __forceinline__ void put_scale(const Linear8Args& g, int m, int b, int byte) {
@@ -92,7 +50,106 @@ __device__ __forceinline__ void put_scale(const Linear8Args& g, int m, int b, in
   if (b == blocks - 1)
     for (int j = blocks; j < g.sld_y8; ++j) row[j] = (unsigned char)scale_byte(0u);
 }
-
+// The residual of an epilogue: none, of one of the types, or (RES_ANY) of the type
+// that the arguments say, for tiles at an edge.
+enum Res { RES_NONE, RES_BF16, RES_FP32, RES_ANY };
+// Eight elements of a residual row, as they lie in memory where the type is known.
+template <int R>
+struct RawRes {
+  typename std::conditional_t<R == RES_BF16, Raw8<bf16_t>, Raw8<float>> raw;
+  __device__ __forceinline__ void load(const Linear8Args& g, long long at, int left) {
+    if constexpr (R == RES_BF16) {
+      raw.load(static_cast<const bf16_t*>(g.res) + at, left);
+    } else if constexpr (R == RES_FP32) {
+      raw.load(static_cast<const float*>(g.res) + at, left);
+    } else if (g.res_fp32) {
+      load8_edge(static_cast<const float*>(g.res) + at, left, raw.w);
+    } else {
+      load8_edge(static_cast<const bf16_t*>(g.res) + at, left, raw.w);
+    }
+  }
+  __device__ __forceinline__ void add(float (&v)[8]) const {
+    float r[8];
+    raw.get(r);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] += r[e];
+  }
+};
+template <bool FULL, bool STRM, typename T>
+__device__ __forceinline__ void store_run(T* p, int left, const float (&v)[8]) {
+  if constexpr (FULL)
+    store8<STRM>(p, v);
+  else
+    store8_edge<STRM>(p, left, v);
+}
+// COUNT runs of eight columns of the epilogue, from the sums v of rows m to the
+// results; nothing is rounded on the way but for the z that is kept.  Each step
+// is done for all runs, so that its branches (the same for all lanes) stand
+// around independent work.  FULL: no row or column lies past the last one.
+template <bool FULL, bool STRM, typename Y, int R, int COUNT>
+__device__ __forceinline__ void epilogue_runs(const Linear8Args& g, const int (&m)[COUNT], int n,
+                                              const float (&bias)[8],
+                                              const RawRes<R> (&res)[COUNT],
+                                              float (&v)[COUNT][8]) {
+  const int left = g.n - n;
+  // for an 8-bit result a run past the last column pads the last block
+  const bool cols = FULL || (is8<Y> ? n < g.ld_y8 : left > 0);
+#pragma unroll
+  for (int s = 0; s < COUNT; ++s)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[s][e] += bias[e];
+  if (g.z) {
+    auto* z = static_cast<KeptOf<Y>*>(g.z) + n;
+#pragma unroll
+    for (int s = 0; s < COUNT; ++s)
+      if (FULL || (cols && m[s] < g.m)) store_run<FULL, STRM>(z + (long long)m[s] * g.ldz, left, v[s]);
+  }
+  activate(v, g.act);
+  if (R != RES_NONE && g.res) {
+#pragma unroll
+    for (int s = 0; s < COUNT; ++s) res[s].add(v[s]);
+  }
+  if constexpr (is8<Y>) {
+#pragma unroll
+    for (int s = 0; s < COUNT; ++s) {
+      if (!FULL) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[s][e] = e < left ? v[s][e] : 0.f;
+      }
+      const int byte = block_units(v[s], v[s]);
+      if (FULL || (cols && m[s] < g.m)) {
+        *reinterpret_cast<u32x2_t*>(g.y8 + (long long)m[s] * g.ld_y8 + n) = to_e4m3(v[s]);
+        if ((n & 127) == 0) put_scale(g, m[s], n >> 7, byte);
+      }
+    }
+  } else {
+    Y* y = static_cast<Y*>(g.y) + n;
+#pragma unroll
+    for (int s = 0; s < COUNT; ++s)
+      if (FULL || (cols && m[s] < g.m)) store_run<FULL, STRM>(y + (long long)m[s] * g.ldy, left, v[s]);
+  }
+}
+// The same for four columns; any of them may lie past the last one.
+template <typename Y>
+__device__ __forceinline__ void epilogue4(const Linear8Args& g, int m, int n, f32x4_t& s) {
+  float v[1][4] = {{s[0], s[1], s[2], s[3]}};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (g.bias && n + e < g.n) v[0][e] += g.bias[n + e];
+    if (g.z && n + e < g.n)
+      static_cast<KeptOf<Y>*>(g.z)[(long long)m * g.ldz + n + e] = from_f32<KeptOf<Y>>(v[0][e]);
+  }
+  activate(v, g.act);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (g.res && n + e < g.n) {
+      const long long at = (long long)m * g.ldr + n + e;
+      v[0][e] += g.res_fp32 ? static_cast<const float*>(g.res)[at]
+                            : to_f32(static_cast<const bf16_t*>(g.res)[at]);
+    }
+    s[e] = v[0][e];
+  }
+}
 // ---------------------------------------------------------------- tiles
 // A workgroup computes BN columns n (the MFMA's rows, operand b) by BM rows m
 // (its columns, operand a) of y.  k advances by one block of 128 per k-tile:
@@ -123,7 +180,8 @@ __device__ __forceinline__ void put_scale(const Linear8Args& g, int m, int b, in
 //   GHz: it is bound by power.  Without the stores of y it would take 752 us.
 //   4 waves of 128 x 128, 512 registers each: 110 us; 4 stages of 64 k: 116 us.
 template <int BM, int BN, int WGM, int WGN, bool EXACT, bool STRM, typename Y, bool EPI = false>
-__global__ __launch_bounds__(64 * WGM * WGN) void matmul8_tile_kernel(ProductArgs<EPI> g) {
+__global__ __launch_bounds__(64 * WGM * WGN, WGM * WGN == 8 && BM == 128 ? 4 : 1) void
+matmul8_tile_kernel(ProductArgs<EPI> g) {
   constexpr int NW = WGM * WGN;
   constexpr int WTM = BM / WGM, WTN = BN / WGN;
   constexpr int FM = WTM / 32, FN = WTN / 32;
@@ -138,7 +196,8 @@ __global__ __launch_bounds__(64 * WGM * WGN) void matmul8_tile_kernel(ProductArg
                 "one operand's scales per wave");
   static_assert(FN % 2 == 0, "halves of a wave's columns are staged");
   __shared__ u32x4_t S0[STAGE], S1[STAGE];
-  __shared__ unsigned C0[BM + BN], C1[BM + BN];
+  __shared__ __attribute__((aligned(16))) unsigned C0[BM + BN];
+  __shared__ unsigned C1[BM + BN];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave / WGN, wn = wave % WGN;
@@ -327,65 +386,123 @@ __global__ __launch_bounds__(64 * WGM * WGN) void matmul8_tile_kernel(ProductArg
     else
       asm volatile("" ::: "memory");
   };
-  Y* y = static_cast<Y*>(g.y);
   constexpr int HALVES = is8<Y> ? 1 : 2, FH = FN / HALVES;
+  constexpr int RUNS = 32 * RPR / 64 / WPG;  // of a lane, per staged part
   const int n_part = n0 + (is8<Y> ? wn / WPG * 128 : wn * WTN);
-  float bias[HALVES][8];
-  if constexpr (EPI) {
+  auto stage = [&](int j, int h) __attribute__((always_inline)) {
 #pragma unroll
-    for (int h = 0; h < HALVES; ++h) {
-      const int n = n_part + h * HC + 8 * (lane % RPR);
-      load8_edge(g.bias ? g.bias + n : nullptr, g.bias ? g.n - n : 0, bias[h]);
-    }
-  }
+    for (int i = 0; i < FH; ++i)
 #pragma unroll
-  for (int j = 0; j < FM; ++j)
-#pragma unroll
-    for (int h = 0; h < HALVES; ++h) {
-#pragma unroll
-      for (int i = 0; i < FH; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const f32x16_t& c = acc[h * FH + i][j];
-          *reinterpret_cast<f32x4_t*>(T + unit(lane & 31, sub * (WTN / 4) + 8 * i + 2 * q + hsel)) =
-              f32x4_t{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
-        }
-      staged();
-#pragma unroll
-      for (int s = 0; s < 32 * RPR / 64 / WPG; ++s) {
-        const int t = lane + 64 * (s * WPG + sub), rr = t / RPR, c = t % RPR;
-        float v[8];
-        const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(T + unit(rr, 2 * c));
-        const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(T + unit(rr, 2 * c + 1));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[e] = lo[e];
-          v[4 + e] = hi[e];
-        }
-        const int m = m0 + wm * WTM + j * 32 + rr, n = n_part + h * HC + 8 * c;
-        if constexpr (is8<Y>) {
-          // 16 lanes have a row's block: they stay together
-          if (m < g.m && n_part < g.n) {
-            epilogue8<STRM, Y>(g, m, n, bias[h], v);
-            unsigned top = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if (n + e >= g.n) v[e] = 0.f;
-              const unsigned f = finite_bits(v[e]);
-              top = top > f ? top : f;
-            }
-            const int byte = scale_byte(max16(top));
-            to_units(v, byte, v);
-            *reinterpret_cast<u32x2_t*>(g.y8 + (long long)m * g.ld_y8 + n) = to_e4m3(v);
-            if (c == 0) put_scale(g, m, n >> 7, byte);
-          }
-        } else if (m < g.m) {
-          if constexpr (EPI) epilogue8<STRM, Y>(g, m, n, bias[h], v);
-          store8_edge<STRM>(y + (long long)m * g.ldy + n, g.n - n, v);
-        }
+      for (int q = 0; q < 4; ++q) {
+        const f32x16_t& c = acc[h * FH + i][j];
+        *reinterpret_cast<f32x4_t*>(T + unit(lane & 31, sub * (WTN / 4) + 8 * i + 2 * q + hsel)) =
+            f32x4_t{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
       }
-      staged();
+    staged();
+  };
+  // run s of the lane: its row and column of the part, and its sums
+  auto row_of = [&](int s) { return (lane + 64 * (s * WPG + sub)) / RPR; };
+  const int c_run = 8 * (lane % RPR);
+  auto take = [&](int s, float (&v)[8]) __attribute__((always_inline)) {
+    const int rr = row_of(s);
+    const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(T + unit(rr, c_run / 4));
+    const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(T + unit(rr, c_run / 4 + 1));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      v[e] = lo[e];
+      v[4 + e] = hi[e];
     }
+  };
+  if constexpr (!EPI) {
+    Y* y = static_cast<Y*>(g.y);
+#pragma unroll
+    for (int j = 0; j < FM; ++j)
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) {
+        stage(j, h);
+#pragma unroll
+        for (int s = 0; s < RUNS; ++s) {
+          float v[8];
+          take(s, v);
+          const int m = m0 + wm * WTM + j * 32 + row_of(s), n = n_part + h * HC + c_run;
+          if (m < g.m) store8_edge<STRM>(y + (long long)m * g.ldy + n, g.n - n, v);
+        }
+        staged();
+      }
+  } else {
+    // The bias of the tile's columns, in LDS: a load from memory behind the stores
+    // of a run would wait for them.
+    float* Cb = reinterpret_cast<float*>(C0);
+    for (int i = tid; i < BN; i += 64 * NW)
+      Cb[i] = g.bias && n0 + i < g.n ? g.bias[n0 + i] : 0.f;
+    __syncthreads();
+    // One copy of the code for all parts: only the staging names accumulators.
+    constexpr int COUNT = 2, STEPS = FM * HALVES * RUNS / COUNT;
+    static_assert(RUNS % COUNT == 0 && STEPS % 2 == 0, "pairs of steps");
+    auto finish = [&](auto full, auto res_kind) __attribute__((always_inline)) {
+      constexpr bool FULL = decltype(full)::value;
+      constexpr int R = decltype(res_kind)::value;
+      constexpr bool AHEAD = R == RES_BF16 || R == RES_FP32;
+      // The residual of the lane's runs t, t + 1, .. is on its way a step before it is
+      // used, in one of two sets of registers: a copy from one to the other would wait
+      // for it, and for the stores of the step before.
+      RawRes<R> even[COUNT], odd[COUNT];
+      auto fetch = [&](int t, RawRes<R>(&res)[COUNT]) __attribute__((always_inline)) {
+        const int p = t / RUNS, n = n_part + p % HALVES * HC + c_run;
+#pragma unroll
+        for (int s = 0; s < COUNT; ++s) {
+          const int m = m0 + wm * WTM + p / HALVES * 32 + row_of(t % RUNS + s);
+          if (FULL || (m < g.m && n < g.n)) res[s].load(g, (long long)m * g.ldr + n, FULL ? 8 : g.n - n);
+        }
+      };
+      auto step = [&](int t, RawRes<R>(&res)[COUNT]) __attribute__((always_inline)) {
+        const int p = t / RUNS, b = t % RUNS;
+        const int n = n_part + p % HALVES * HC + c_run;
+        if (R == RES_ANY && g.res) fetch(t, res);
+        float bias[8];
+        const f32x4_t* bl = reinterpret_cast<const f32x4_t*>(Cb + (n - n0));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) bias[e] = bl[e / 4][e % 4];
+        if (b == 0) {
+          if (t > 0) staged();
+          static_for<FM * HALVES>([&](auto q) {
+            if (p == q) stage(decltype(q)::value / HALVES, decltype(q)::value % HALVES);
+          });
+        }
+        int m[COUNT];
+        float v[COUNT][8];
+#pragma unroll
+        for (int s = 0; s < COUNT; ++s) {
+          m[s] = m0 + wm * WTM + p / HALVES * 32 + row_of(b + s);
+          take(b + s, v[s]);
+        }
+        epilogue_runs<FULL, STRM, Y, R>(g, m, n, bias, res, v);
+      };
+      if constexpr (AHEAD) {
+        fetch(0, even);
+#pragma unroll 1
+        for (int t = 0; t < STEPS * COUNT; t += 2 * COUNT) {
+          fetch(t + COUNT, odd);
+          step(t, even);
+          // (after the last pair the first runs again, unused)
+          fetch(t + 2 * COUNT < STEPS * COUNT ? t + 2 * COUNT : 0, even);
+          step(t + COUNT, odd);
+        }
+      } else {
+#pragma unroll 1
+        for (int t = 0; t < STEPS * COUNT; t += COUNT) step(t, even);
+      }
+    };
+    using Whole = std::true_type;
+    if (m0 + BM > g.m || n0 + BN > g.n)
+      finish(std::false_type{}, std::integral_constant<int, RES_ANY>{});
+    else if (!g.res)
+      finish(Whole{}, std::integral_constant<int, RES_NONE>{});
+    else if (g.res_fp32)
+      finish(Whole{}, std::integral_constant<int, RES_FP32>{});
+    else
+      finish(Whole{}, std::integral_constant<int, RES_BF16>{});
+  }
 }
 
 // ---------------------------------------------------------------- rows

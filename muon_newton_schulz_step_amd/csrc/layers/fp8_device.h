@@ -184,6 +184,19 @@ __device__ __forceinline__ unsigned max16(unsigned u) {
   return u;
 }
 
+// Sum over each row of 16 lanes, in all of them.
+__device__ __forceinline__ float sum16(float v) {
+  auto step = [&](auto ctrl) {
+    v += __uint_as_float((unsigned)__builtin_amdgcn_update_dpp(
+        0, (int)__float_as_uint(v), decltype(ctrl)::value, 0xf, 0xf, false));
+  };
+  step(std::integral_constant<int, 0x128>{});  // row_ror:8
+  step(std::integral_constant<int, 0x124>{});
+  step(std::integral_constant<int, 0x122>{});
+  step(std::integral_constant<int, 0x121>{});
+  return v;
+}
+
 // Sum over the wave, the same in all lanes and from run to run: DPP adds inside
 // rows of 16 lanes, then across the rows; lane 63 ends up with the total.
 __device__ __forceinline__ float wave_sum(float v) {

@@ -21,59 +21,94 @@
 
 namespace muon {
 
-// The sums over a row that two norms take one after the other: each call uses the
-// other of two buffers, so one barrier per call is enough.
-template <int TEAM, int N>
-struct TeamSums {
-  float (*buf)[N][16];
-  int turn;
-  template <int M>
-  __device__ __forceinline__ void operator()(float (&v)[M], int tw, int lane) {
-    static_assert(M <= N, "buffer");
-    team_sum<TEAM>(v, buf[turn], tw, lane);
-    turn ^= 1;
+// Columns of a row that wave w of a team has.
+template <int TEAM, int NCH>
+__device__ __forceinline__ float columns_of(int w, int cols) {
+  int c = 0;
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) {
+    const int left = cols - (k * TEAM + w) * 512;
+    c += left < 0 ? 0 : left < 512 ? left : 512;
   }
-};
+  return (float)c;
+}
 
-// A row's mean and 1 / sqrt(variance + eps); x becomes the deviations.  The mean's
-// own rounding is taken out by the sum of the deviations, as layer norm of fp32
-// rows does it.
-template <int NCH, typename Sums>
-__device__ __forceinline__ void row_norm(float (&x)[NCH][8], const int (&col)[NCH], int cols, float n,
-                                         bool rms, float eps, Sums& sums, int tw, int lane, float& mu,
-                                         float& rstd) {
+// A row's mean and 1 / sqrt(variance + eps); x becomes the deviations.  Each wave
+// takes the mean of its own columns and the squared deviations from that, corrected
+// by the sum of the deviations (which are the mean's rounding), and the team joins
+// them behind one barrier: with c_w columns, mean m_w and sum M_w of wave w
+//   mean = m_0 + sum c_w (m_w - m_0) / n,  sum = sum M_w + c_w (m_w - mean)^2,
+// so that a row of equal values has that value as its mean, exactly.  Lane l of each
+// row of 16 takes wave l's part (`share`: its columns).  `buf` alternates between calls.
+template <int TEAM, int NCH>
+__device__ __forceinline__ void row_norm(float (&x)[NCH][8], const int (&col)[NCH], int cols, bool rms,
+                                         float eps, float (*buf)[16], int tw, int lane, float own,
+                                         float share, float& mu, float& rstd) {
+  const float n = (float)cols;
+  float t[2] = {0.f, 0.f};
   mu = 0.f;
-  if (!rms) {
-    float s[1] = {0.f};
+  if (rms) {
 #pragma unroll
     for (int k = 0; k < NCH; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[0] += x[k][i];
-    sums(s, tw, lane);
-    mu = s[0] / n;
+      for (int i = 0; i < 8; ++i) t[0] = fmaf(x[k][i], x[k][i], t[0]);
+    float q[1] = {t[0]};
+    team_sum<TEAM>(q, buf, tw, lane);
+    rstd = 1.f / sqrtf(q[0] / n + eps);
+    return;
   }
-  float t[2] = {0.f, 0.f};
+  float s = 0.f;
 #pragma unroll
   for (int k = 0; k < NCH; ++k)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float d = col[k] + i < cols ? x[k][i] - mu : 0.f;
-      t[0] = fmaf(d, d, t[0]);
-      t[1] += d;
+    for (int i = 0; i < 8; ++i) s += x[k][i];
+  const float inv = own > 0.f ? 1.f / own : 0.f;
+  float m = wave_sum(s) * inv;
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) {
+    const int left = cols - col[k];
+    if (left >= 8) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = x[k][i] - m;
+        t[0] = fmaf(d, d, t[0]);
+        t[1] += d;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float d = i < left ? x[k][i] - m : 0.f;
+        t[0] = fmaf(d, d, t[0]);
+        t[1] += d;
+      }
     }
-  sums(t, tw, lane);
-  float var = t[0] / n;
-  if (!rms) {
-    const float off = t[1] / n, better = mu + off;
-    mu = better == better ? better : mu;  // (an infinite mean stays one)
-    var -= off * off;
-    var = var < 0.f ? 0.f : var;
-#pragma unroll
-    for (int k = 0; k < NCH; ++k)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[k][i] -= mu;
   }
-  rstd = 1.f / sqrtf(var + eps);
+  t[0] = wave_sum(t[0]);
+  t[1] = wave_sum(t[1]);
+  const float off = t[1] * inv, better = m + off;
+  m = better == better ? better : m;  // (an infinite mean stays one)
+  t[0] = fmaf(-t[1], off, t[0]);
+  t[0] = t[0] < 0.f ? 0.f : t[0];
+  mu = m;
+  float sum = t[0];
+  if constexpr (TEAM > 1) {
+    if (lane == 0) {
+      buf[0][tw] = m;
+      buf[1][tw] = t[0];
+    }
+    __syncthreads();
+    const int l = lane & 15;
+    const float m0 = buf[0][0], ml = buf[0][l < TEAM ? l : 0], ql = buf[1][l < TEAM ? l : 0];
+    mu = m0 + sum16(l < TEAM ? share * (ml - m0) : 0.f) / n;
+    if (mu != mu) mu = sum16(l < TEAM ? share * ml : 0.f) / n;  // an infinite mean, as the formula has it
+    const float e = ml - mu;
+    sum = sum16(l < TEAM ? fmaf(share * e, e, ql) : 0.f);
+  }
+#pragma unroll
+  for (int k = 0; k < NCH; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[k][i] -= mu;
+  rstd = 1.f / sqrtf(sum / n + eps);
 }
 
 constexpr int forward_waves(int team) { return team > 1 ? team : 4; }
@@ -84,35 +119,47 @@ __global__ __launch_bounds__(64 * forward_waves(TEAM)) void residual_norm_kernel
   using B = typename ElemOf<BT>::type;
   constexpr int TEAMS = forward_waves(TEAM) / TEAM;
   __shared__ float buf[2][2][16];
-  TeamSums<TEAM, 2> sums{buf, 0};
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int tw = wave % TEAM;
   const long long step = (long long)gridDim.x * TEAMS;
   const bool post = a.p.post_weight, rms = a.p.rms;
-  const float s = a.p.scale ? *a.p.scale : 1.f, n = (float)a.cols;
+  const float s = a.p.scale ? *a.p.scale : 1.f;
+  const float own = columns_of<TEAM, NCH>(tw, a.cols), share = columns_of<TEAM, NCH>(lane & 15, a.cols);
+  // rows too long for the registers have their vectors read again for each row
+  constexpr bool LEAN = TEAM * NCH > 16;
   int col[NCH];
-  float w[NCH][8], b[NCH][8], pw[NCH][8], pb[NCH][8];  // pw, pb times the gate
+  float w[LEAN ? 1 : NCH][8], b[LEAN ? 1 : NCH][8];
+  float pw[LEAN ? 1 : NCH][8], pb[LEAN ? 1 : NCH][8];  // times the gate
+  // columns past the last one have zeros everywhere: nothing below asks for them
   auto vec = [&](const float* p, int c, float otherwise, float (&v)[8]) __attribute__((always_inline)) {
     if (p) {
       load8_edge(p + c, a.cols - c, v);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = otherwise;
+      for (int i = 0; i < 8; ++i) v[i] = c + i < a.cols ? otherwise : 0.f;
+    }
+  };
+  auto vectors_in = [&](int c, float (&w)[8], float (&b)[8]) __attribute__((always_inline)) {
+    vec(a.p.weight, c, 1.f, w);
+    vec(a.p.bias, c, 0.f, b);
+  };
+  auto vectors_post = [&](int c, float (&pw)[8], float (&pb)[8]) __attribute__((always_inline)) {
+    float gate[8];
+    vec(a.p.gate, c, 1.f, gate);
+    vec(a.p.post_weight, c, 1.f, pw);
+    vec(a.p.post_bias, c, 0.f, pb);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      pw[i] *= gate[i];
+      pb[i] *= gate[i];
     }
   };
 #pragma unroll
   for (int k = 0; k < NCH; ++k) {
     col[k] = ((k * TEAM + tw) * 64 + lane) * 8;
-    float gate[8];
-    vec(a.p.weight, col[k], 1.f, w[k]);
-    vec(a.p.bias, col[k], 0.f, b[k]);
-    vec(a.p.gate, col[k], 1.f, gate);
-    vec(a.p.post_weight, col[k], 1.f, pw[k]);
-    vec(a.p.post_bias, col[k], 0.f, pb[k]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      pw[k][i] *= gate[i];
-      pb[k][i] *= gate[i];
+    if constexpr (!LEAN) {
+      vectors_in(col[k], w[k], b[k]);
+      vectors_post(col[k], pw[k], pb[k]);
     }
   }
   Raw8<X> rx[NCH];
@@ -124,6 +171,7 @@ __global__ __launch_bounds__(64 * forward_waves(TEAM)) void residual_norm_kernel
       if (a.b) rb[k].load(static_cast<const B*>(a.b) + row * a.ldb + col[k], a.cols - col[k]);
     }
   };
+  int turn = 0;
   long long row = (long long)blockIdx.x * TEAMS + wave / TEAM;
   if (row < a.rows) fetch(row);
   for (; row < a.rows; row += step) {
@@ -140,18 +188,21 @@ __global__ __launch_bounds__(64 * forward_waves(TEAM)) void residual_norm_kernel
     }
     if (row + step < a.rows) fetch(row + step);
     float pmu = 0.f, prstd = 1.f;
-    if (post) row_norm(v, col, a.cols, n, rms, a.p.eps, sums, tw, lane, pmu, prstd);
+    if (post)
+      row_norm<TEAM>(v, col, a.cols, rms, a.p.eps, buf[0], tw, lane, own, share, pmu, prstd);
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
+      constexpr int ONE = LEAN ? 0 : 1;
+      if constexpr (LEAN) vectors_post(col[k], pw[0], pb[0]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float p = fmaf(v[k][i] * prstd, pw[k][i], pb[k][i]);
-        v[k][i] = col[k] + i < a.cols ? fmaf(s, x[k][i], p) : 0.f;
-      }
+      for (int i = 0; i < 8; ++i)
+        v[k][i] = fmaf(s, x[k][i], fmaf(v[k][i] * prstd, pw[k * ONE][i], pb[k * ONE][i]));
       if (a.r) store8_edge(static_cast<X*>(a.r) + row * a.ldr + col[k], a.cols - col[k], v[k]);
     }
     float mu, rstd;
-    row_norm(v, col, a.cols, n, rms, a.p.eps, sums, tw, lane, mu, rstd);
+    row_norm<TEAM>(v, col, a.cols, rms, a.p.eps, buf[post ? 1 : turn], tw, lane, own, share, mu,
+                   rstd);
+    turn ^= 1;
     if (tw == 0 && lane == 0) {
       a.stats[row] = mu;
       a.stats[a.rows + row] = rstd;
@@ -161,18 +212,16 @@ __global__ __launch_bounds__(64 * forward_waves(TEAM)) void residual_norm_kernel
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       float y[8];
+      constexpr int ONE = LEAN ? 0 : 1;
+      if constexpr (LEAN) vectors_in(col[k], w[0], b[0]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = fmaf(v[k][i] * rstd, w[k][i], b[k][i]);
+      for (int i = 0; i < 8; ++i) y[i] = fmaf(v[k][i] * rstd, w[k * ONE][i], b[k * ONE][i]);
       if (a.h_type == kOut8) {
-        unsigned top = 0;
+        if (a.cols - col[k] < 8) {  // (a row that is not finite has NaN there)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (col[k] + i >= a.cols) y[i] = 0.f;
-          const unsigned f = finite_bits(y[i]);
-          top = top > f ? top : f;
+          for (int i = 0; i < 8; ++i) y[i] = col[k] + i < a.cols ? y[i] : 0.f;
         }
-        const int byte = scale_byte(max16(top));
-        to_units(y, byte, y);
+        const int byte = block_units(y, y);
         if (col[k] < a.ld) *reinterpret_cast<u32x2_t*>(a.h8 + row * a.ld + col[k]) = to_e4m3(y);
         const unsigned word = pack_scales(byte);
         const int piece = k * TEAM + tw;
@@ -187,17 +236,30 @@ __global__ __launch_bounds__(64 * forward_waves(TEAM)) void residual_norm_kernel
   }
 }
 
-// Waves of a backward workgroup: whole teams, about eight.
-constexpr int back_waves(int team) { return team > 8 ? team : 8 / team * team; }
+// Waves of a backward workgroup, of which a CU holds one: whole teams, as many as
+// the registers allow (up to 170 a lane for 12, 128 for 16).
+constexpr int back_waves(int team, bool branch, bool fp32) {
+  const int most = !branch ? 16 : fp32 ? 8 : 12;
+  return team >= 8 ? team : most / team * team;
+}
+// Where a lane has 16 columns their sums do not fit its registers: as many of them
+// as there is room for are kept in LDS.
+constexpr int back_lds(int team, int nch, bool branch) {
+  return nch == 1 ? 0 : team == 16 ? 2 : branch ? 4 : 0;
+}
 
 // A team without a row left still takes part in the workgroup's barriers.
 template <int XT, int BT, int TEAM, int NCH, bool BRANCH>
-__global__ __launch_bounds__(64 * back_waves(TEAM)) void residual_back_kernel(ResidualBackArgs a) {
+__global__ __launch_bounds__(64 * back_waves(TEAM, BRANCH, BT == MUON_FP32)) void
+residual_back_kernel(ResidualBackArgs a) {
   using X = typename ElemOf<XT>::type;
   using B = typename ElemOf<BT>::type;
-  constexpr int WAVES = back_waves(TEAM), TEAMS = WAVES / TEAM, K = BRANCH ? 4 : 2;
-  // fp32 rows of several chunks leave no room for the next one
-  constexpr bool EARLY = XT == MUON_BF16 || NCH == 1;
+  constexpr int WAVES = back_waves(TEAM, BRANCH, BT == MUON_FP32), TEAMS = WAVES / TEAM;
+  constexpr int K = BRANCH ? 4 : 2, LDS = back_lds(TEAM, NCH, BRANCH);
+  // rows too long for the registers have their vectors read again for each row, and
+  // their next one, as fp32 rows of several chunks, when its turn comes
+  constexpr bool LEAN = TEAM * NCH > 16;
+  constexpr bool EARLY = NCH == 1 || (XT == MUON_BF16 && !LEAN);
   __shared__ float buf[2][TEAMS][2][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int tw = wave % TEAM, team = wave / TEAM;
@@ -205,27 +267,55 @@ __global__ __launch_bounds__(64 * back_waves(TEAM)) void residual_back_kernel(Re
   const bool post = a.p.post_weight;
   const float s = a.p.scale ? *a.p.scale : 1.f, n = (float)a.cols, centre = a.p.rms ? 0.f : 1.f / n;
   int col[NCH];
-  float w[NCH][8], wp[BRANCH ? NCH : 1][8];  // wp: post weight times gate
-  float sum[K][NCH][8];                      // dh rh, dh, d bh, d
-  double dscale = 0.0;
+  float w[LEAN ? 1 : NCH][8], wp[BRANCH && !LEAN ? NCH : 1][8];  // wp: post weight times gate
+  // sums of dh rh, dh, d bh, d: in registers or, four columns of a lane side by side
+  // with its neighbours', in LDS
+  float reg_sum[LDS < K ? K - LDS : 1][NCH][8];
+  __shared__ f32x4_t lds_sum[LDS ? LDS * NCH * 2 * 64 * WAVES : 1];
+  f32x4_t* own = lds_sum + threadIdx.x;
+  auto add = [&](auto j, auto k, const float (&v)[8]) __attribute__((always_inline)) {
+    constexpr int J = decltype(j)::value, C = decltype(k)::value;
+    if constexpr (J < LDS) {
 #pragma unroll
-  for (int k = 0; k < NCH; ++k) {
-    col[k] = ((k * TEAM + tw) * 64 + lane) * 8;
-    load8_edge(a.p.weight + col[k], a.cols - col[k], w[k]);
+      for (int q = 0; q < 2; ++q) {
+        f32x4_t& s = own[((J * NCH + C) * 2 + q) * 64 * WAVES];
+        f32x4_t t = s;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+        for (int e = 0; e < 4; ++e) t[e] += v[4 * q + e];
+        s = t;
+      }
+    } else {
 #pragma unroll
-      for (int j = 0; j < K; ++j) sum[j][k][i] = 0.f;
-    if constexpr (BRANCH) {
-      float g[8], p[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = p[i] = col[k] + i < a.cols ? 1.f : 0.f;
-      if (a.p.gate) load8_edge(a.p.gate + col[k], a.cols - col[k], g);
-      if (post) load8_edge(a.p.post_weight + col[k], a.cols - col[k], p);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) wp[k][i] = g[i] * p[i];
+      for (int i = 0; i < 8; ++i) reg_sum[J - LDS][C][i] += v[i];
     }
-  }
+  };
+  double dscale = 0.0;
+  auto branch_weight = [&](int c, float (&v)[8]) __attribute__((always_inline)) {
+    float g[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = g[i] = c + i < a.cols ? 1.f : 0.f;
+    if (a.p.gate) load8_edge(a.p.gate + c, a.cols - c, g);
+    if (post) load8_edge(a.p.post_weight + c, a.cols - c, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= g[i];
+  };
+  static_for<NCH>([&](auto kk) {
+    constexpr int k = decltype(kk)::value;
+    col[k] = ((k * TEAM + tw) * 64 + lane) * 8;
+    static_for<K>([&](auto jj) {
+      constexpr int j = decltype(jj)::value;
+      if constexpr (j < LDS) {
+        own[((j * NCH + k) * 2) * 64 * WAVES] = own[((j * NCH + k) * 2 + 1) * 64 * WAVES] = f32x4_t{};
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) reg_sum[j - LDS][k][i] = 0.f;
+      }
+    });
+    if constexpr (!LEAN) {
+      load8_edge(a.p.weight + col[k], a.cols - col[k], w[k]);
+      if constexpr (BRANCH) branch_weight(col[k], wp[k]);
+    }
+  });
   Raw8<X> rr[NCH], rdr[NCH], rx[NCH];
   Raw8<B> rdh[NCH], rb[NCH];
   float st[4] = {0.f, 0.f, 0.f, 0.f};
@@ -241,6 +331,13 @@ __global__ __launch_bounds__(64 * back_waves(TEAM)) void residual_back_kernel(Re
       const int left = a.cols - col[k];
       rr[k].load(static_cast<const X*>(a.r) + row * a.ldr + col[k], left);
       rdh[k].load(static_cast<const B*>(a.dh) + row * a.lddh + col[k], left);
+    }
+  };
+  // what is not used before the first sums are known
+  auto fetch_late = [&](long long row) __attribute__((always_inline)) {
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int left = a.cols - col[k];
       if (a.dr) rdr[k].load(static_cast<const X*>(a.dr) + row * a.lddr + col[k], left);
       if (BRANCH) rb[k].load(static_cast<const B*>(a.b) + row * a.ldb + col[k], left);
       if (a.g.scale) rx[k].load(static_cast<const X*>(a.x) + row * a.ldx + col[k], left);
@@ -248,67 +345,89 @@ __global__ __launch_bounds__(64 * back_waves(TEAM)) void residual_back_kernel(Re
   };
   int turn = 0;
   long long first = (long long)blockIdx.x * TEAMS;  // of the workgroup's teams
-  if (EARLY && first + team < a.rows) fetch(first + team);
+  if (EARLY && first + team < a.rows) {
+    fetch(first + team);
+    fetch_late(first + team);
+  }
   for (; first < a.rows; first += step) {
     const long long row = first + team;
     const bool in = row < a.rows;
-    if (!EARLY && in) fetch(row);
+    if (!EARLY && in) {
+      fetch(row);
+      if (!LEAN) fetch_late(row);
+    }
     const float mu = st[0], r = st[1], pmu = st[2], pr = post ? st[3] : 1.f;
-    float x[NCH][8], d[NCH][8], dr[NCH][8], bh[BRANCH ? NCH : 1][8];
+    float x[NCH][8], d[NCH][8], bh[BRANCH ? NCH : 1][8];
     float c[2] = {0.f, 0.f};
     float ds = 0.f;
     if (in) {
-#pragma unroll
-      for (int k = 0; k < NCH; ++k) {
+      static_for<NCH>([&](auto kk) {
+        constexpr int k = decltype(kk)::value;
         rr[k].get(x[k]);
         rdh[k].get(d[k]);
-        if (a.dr) {
-          rdr[k].get(dr[k]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) dr[k][i] = 0.f;
-        }
-        if constexpr (BRANCH) rb[k].get(bh[k]);
+        float p[8];
+        add(std::integral_constant<int, 1>{}, kk, d[k]);
+        constexpr int kw = LEAN ? 0 : k;
+        if constexpr (LEAN) load8_edge(a.p.weight + col[k], a.cols - col[k], w[0]);
+        // past the last column dh, x and the weights are zeros, so whatever rh and
+        // bh come to there, no sum over the row gets anything from it
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float rh = col[k] + i < a.cols ? (x[k][i] - mu) * r : 0.f;
-          sum[0][k][i] = fmaf(d[k][i], rh, sum[0][k][i]);
-          sum[1][k][i] += d[k][i];
-          const float g = d[k][i] * w[k][i];
+          const float rh = (x[k][i] - mu) * r;
+          p[i] = d[k][i] * rh;
+          const float g = d[k][i] * w[kw][i];
           c[0] += g;
           c[1] = fmaf(g, rh, c[1]);
           x[k][i] = rh;
           d[k][i] = g;
         }
-      }
+        add(std::integral_constant<int, 0>{}, kk, p);
+      });
     }
     team_sum<TEAM>(c, buf[turn][team], tw, lane);
     turn ^= 1;
     float e[2] = {0.f, 0.f};
     if (in) {
       const float c0 = c[0] * centre, c1 = c[1] / n;
-#pragma unroll
-      for (int k = 0; k < NCH; ++k) {
-        float xs[8];
+      if (LEAN) fetch_late(row);
+      static_for<NCH>([&](auto kk) {
+        constexpr int k = decltype(kk)::value;
+        float xs[8], p[8];
+        constexpr int kw = LEAN || !BRANCH ? 0 : k;
+        if constexpr (LEAN && BRANCH) branch_weight(col[k], wp[0]);
         if (a.g.scale) rx[k].get(xs);
+        float dr[8];
+        if (a.dr) {
+          rdr[k].get(dr);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dr[i] = 0.f;
+        }
+        if constexpr (BRANCH) rb[k].get(bh[k]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float v = fmaf(r, d[k][i] - c0 - x[k][i] * c1, dr[k][i]);
+          const float v = fmaf(r, d[k][i] - c0 - x[k][i] * c1, dr[i]);
           if (a.g.scale) ds = fmaf(v, xs[i], ds);
           d[k][i] = v;
           if constexpr (BRANCH) {
-            const float h = col[k] + i < a.cols ? (bh[k][i] - pmu) * pr : 0.f;
-            sum[2][k][i] = fmaf(v, h, sum[2][k][i]);
-            sum[3][k][i] += v;
-            const float g = v * wp[k][i];
+            const float h = (bh[k][i] - pmu) * pr;
+            p[i] = v * h;
+            const float g = v * wp[kw][i];
             e[0] += g;
             e[1] = fmaf(g, h, e[1]);
             bh[k][i] = h;
           }
         }
-      }
+        if constexpr (BRANCH) {
+          add(std::integral_constant<int, 2>{}, kk, p);
+          add(std::integral_constant<int, 3>{}, kk, d[k]);
+        }
+      });
       dscale += (double)ds;
-      if (EARLY && row + step < a.rows) fetch(row + step);
+      if (EARLY && row + step < a.rows) {
+        fetch(row + step);
+        fetch_late(row + step);
+      }
 #pragma unroll
       for (int k = 0; k < NCH; ++k) {
         float o[8];
@@ -326,10 +445,12 @@ __global__ __launch_bounds__(64 * back_waves(TEAM)) void residual_back_kernel(Re
 #pragma unroll
       for (int k = 0; k < NCH; ++k) {
         float o[8];
+        constexpr int ONE = LEAN ? 0 : 1;
+        if constexpr (LEAN && BRANCH) branch_weight(col[k], wp[0]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if constexpr (BRANCH) {
-            const float g = d[k][i] * wp[k][i];
+            const float g = d[k][i] * wp[k * ONE][i];
             o[i] = post ? pr * (g - e0 - bh[k][i] * e1) : g;
           } else {
             o[i] = d[k][i];
@@ -339,27 +460,46 @@ __global__ __launch_bounds__(64 * back_waves(TEAM)) void residual_back_kernel(Re
       }
     }
   }
-  // The workgroup's sums: every team's go to LDS (element i of a chunk's lanes side
-  // by side, the rows of 64 padded by one) and are added in the teams' order.
-  constexpr int ROW = 65, PER = NCH * TEAM * 8 * ROW;
-  __shared__ float acc[TEAMS * PER];
+  // The workgroup's sums.  Those of several teams go to LDS one after the other
+  // (element i of a chunk's lanes side by side, the rows of 64 padded by one) and are
+  // added in the teams' order; a single team's are what it has.
   float* part = a.part + (long long)blockIdx.x * K * a.cols;
+  if constexpr (TEAMS == 1) {
+    static_for<K>([&](auto jj) {
+      constexpr int j = decltype(jj)::value;
+      static_for<NCH>([&](auto kk) {
+        constexpr int k = decltype(kk)::value;
+        float v[8];
 #pragma unroll
-  for (int j = 0; j < K; ++j) {
+        for (int i = 0; i < 8; ++i) {
+          if constexpr (j < LDS)
+            v[i] = own[((j * NCH + k) * 2 + i / 4) * 64 * WAVES][i % 4];
+          else
+            v[i] = reg_sum[j - LDS][k][i];
+        }
+        store8_edge(part + (long long)j * a.cols + col[k], a.cols - col[k], v);
+      });
+    });
+  } else {
+    constexpr int ROW = 65, PER = NCH * TEAM * 8 * ROW;
+    __shared__ float acc[TEAMS * PER];
+    static_for<K>([&](auto jj) {
+      constexpr int j = decltype(jj)::value;
 #pragma unroll
-    for (int k = 0; k < NCH; ++k)
+      for (int k = 0; k < NCH; ++k)
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        acc[team * PER + ((k * TEAM + tw) * 8 + i) * ROW + lane] = sum[j][k][i];
-    __syncthreads();
-    for (int c = threadIdx.x; c < a.cols; c += 64 * WAVES) {
-      const int at = ((c >> 9) * 8 + (c & 7)) * ROW + ((c >> 3) & 63);
-      float v = acc[at];
+        for (int i = 0; i < 8; ++i)
+          acc[team * PER + ((k * TEAM + tw) * 8 + i) * ROW + lane] = reg_sum[j][k][i];
+      __syncthreads();
+      for (int c = threadIdx.x; c < a.cols; c += 64 * WAVES) {
+        const int at = ((c >> 9) * 8 + (c & 7)) * ROW + ((c >> 3) & 63);
+        float v = acc[at];
 #pragma unroll
-      for (int t = 1; t < TEAMS; ++t) v += acc[t * PER + at];
-      part[(long long)j * a.cols + c] = v;
-    }
-    __syncthreads();
+        for (int t = 1; t < TEAMS; ++t) v += acc[t * PER + at];
+        part[(long long)j * a.cols + c] = v;
+      }
+      __syncthreads();
+    });
   }
   if (a.g.scale) {
     __shared__ double dbuf[16];
@@ -440,13 +580,23 @@ namespace {
 template <bool BACK, typename F>
 void with_shape(int cols, bool branch, F&& f) {
 #define MUON_SHAPE(T, N) f(std::integral_constant<int, T>{}, std::integral_constant<int, N>{})
-  if (cols <= 512) MUON_SHAPE(1, 1);
-  else if (cols <= 1024) MUON_SHAPE(1, 2);
-  else if (cols <= 1536) MUON_SHAPE(BACK ? 3 : 1, BACK ? 1 : 3);
-  else if (cols <= 2048) MUON_SHAPE(2, 2);
-  else if (cols <= 4096) MUON_SHAPE(4, 2);
-  else if (cols <= 8192) MUON_SHAPE(8, 2);
-  else MUON_SHAPE(16, 2);
+  if constexpr (BACK) {
+    if (cols <= 512) MUON_SHAPE(1, 1);
+    else if (cols <= 1024) MUON_SHAPE(2, 1);
+    else if (cols <= 1536) MUON_SHAPE(3, 1);
+    else if (cols <= 2048) MUON_SHAPE(4, 1);
+    else if (cols <= 4096) MUON_SHAPE(8, 1);
+    else if (cols <= 8192) MUON_SHAPE(8, 2);
+    else MUON_SHAPE(16, 2);
+  } else {
+    if (cols <= 512) MUON_SHAPE(1, 1);
+    else if (cols <= 1024) MUON_SHAPE(2, 1);
+    else if (cols <= 1536) MUON_SHAPE(3, 1);
+    else if (cols <= 2048) MUON_SHAPE(4, 1);
+    else if (cols <= 4096) MUON_SHAPE(8, 1);
+    else if (cols <= 8192) MUON_SHAPE(16, 1);
+    else MUON_SHAPE(16, 2);
+  }
 #undef MUON_SHAPE
 }
 int groups_for(int rows, int teams, int most) {
@@ -468,7 +618,7 @@ int residual_back_groups(int rows, int cols, bool branch) {
   int g = 0;
   with_shape<true>(cols, branch, [&](auto team, auto) {
     constexpr int T = decltype(team)::value;
-    g = groups_for(rows, back_waves(T) / T, 256);
+    g = groups_for(rows, back_waves(T, branch, false) / T, 256);
   });
   return g;
 }
@@ -494,7 +644,7 @@ hipError_t launch_residual_norm_backward(int x_bf16, int b_bf16, const ResidualB
       with_shape<true>(a.cols, branch, [&](auto team, auto nch) {
         constexpr int T = decltype(team)::value, N = decltype(nch)::value;
         constexpr int X = decltype(xt)::value, B = decltype(bt)::value;
-        const dim3 grid(a.groups), block(64 * back_waves(T));
+        const dim3 grid(a.groups), block(64 * back_waves(T, branch, B == MUON_FP32));
         if (branch)
           hipLaunchKernelGGL((residual_back_kernel<X, B, T, N, true>), grid, block, 0, s, a);
         else

@@ -10,7 +10,12 @@
 // small tensors and a few large ones share a launch evenly.  Each workgroup
 // leaves one sum; the finishing launch, or each workgroup of the clipping one,
 // adds those in their order.  The clipping pass goes over its run backwards:
-// what the norm read last is what the last-level cache still holds.
+// what the norm read last is what the last-level cache still holds, and its
+// results are stored past that.
+//   805e6 numbers, fp32: norm 540 us (6.0 TB/s; a copy runs at 5.2), clipped into
+//   bf16 1482 us (5.4 TB/s over two readings and the writing); bf16: norm 273 us
+//   (5.9), clipped 939 us (5.1).  With half the workgroups and cached stores 600,
+//   1573, 275 and 950 us.
 #include "layers/fp8_device.h"
 #include "muon_clip.h"
 
@@ -136,7 +141,7 @@ __global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipLaunch) {
       raw[k].get(v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = v[j] * c * c2;
-      store8_edge(o + e, left_of(left - e), v);
+      store8_edge<true>(o + e, left_of(left - e), v);  // (not read here again)
     }
   };
   for (unsigned at = run.end; at-- > run.begin;) {

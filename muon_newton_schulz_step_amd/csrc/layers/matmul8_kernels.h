@@ -41,14 +41,11 @@ template <typename Y> using KeptOf = std::conditional_t<std::is_same_v<Y, float>
 template <bool EPI> using ProductArgs = std::conditional_t<EPI, Linear8Args, Matmul8Args>;
 template <typename Y> constexpr bool is8 = std::is_same_v<Y, unsigned char>;
 
-// The scale byte of row m's block `b`; the last block's writer fills the row of
-// scales up, as blocks of zeros, so that equal tensors are equal byte by byte.
-__device__ __forceinline__ void put_scale(const Linear8Args& g, int m, int b, int byte) {
-  unsigned char* row = g.s8 + (long long)m * g.sld_y8;
-  row[b] = (unsigned char)byte;
-  const int blocks = (int)(g.ld_y8 >> 7);
-  if (b == blocks - 1)
-    for (int j = blocks; j < g.sld_y8; ++j) row[j] = (unsigned char)scale_byte(0u);
+// What lies behind the last block in a row of scales: blocks of zeros, so that equal
+// tensors are equal byte by byte.
+__device__ __forceinline__ void pad_scales(const Linear8Args& g, int m) {
+  for (long long j = g.ld_y8 >> 7; j < g.sld_y8; ++j)
+    g.s8[(long long)m * g.sld_y8 + j] = (unsigned char)scale_byte(0u);
 }
 // The residual of an epilogue: none, of one of the types, or (RES_ANY) of the type
 // that the arguments say, for tiles at an edge.
@@ -57,15 +54,15 @@ enum Res { RES_NONE, RES_BF16, RES_FP32, RES_ANY };
 template <int R>
 struct RawRes {
   typename std::conditional_t<R == RES_BF16, Raw8<bf16_t>, Raw8<float>> raw;
-  __device__ __forceinline__ void load(const Linear8Args& g, long long at, int left) {
+  __device__ __forceinline__ void load(const void* p, bool fp32, int left) {
     if constexpr (R == RES_BF16) {
-      raw.load(static_cast<const bf16_t*>(g.res) + at, left);
+      raw.load(static_cast<const bf16_t*>(p), left);
     } else if constexpr (R == RES_FP32) {
-      raw.load(static_cast<const float*>(g.res) + at, left);
-    } else if (g.res_fp32) {
-      load8_edge(static_cast<const float*>(g.res) + at, left, raw.w);
+      raw.load(static_cast<const float*>(p), left);
+    } else if (fp32) {
+      load8_edge(static_cast<const float*>(p), left, raw.w);
     } else {
-      load8_edge(static_cast<const bf16_t*>(g.res) + at, left, raw.w);
+      load8_edge(static_cast<const bf16_t*>(p), left, raw.w);
     }
   }
   __device__ __forceinline__ void add(float (&v)[8]) const {
@@ -82,27 +79,44 @@ __device__ __forceinline__ void store_run(T* p, int left, const float (&v)[8]) {
   else
     store8_edge<STRM>(p, left, v);
 }
-// COUNT runs of eight columns of the epilogue, from the sums v of rows m to the
-// results; nothing is rounded on the way but for the z that is kept.  Each step
-// is done for all runs, so that its branches (the same for all lanes) stand
-// around independent work.  FULL: no row or column lies past the last one.
+// A lane's place in the matrices of the epilogue: its pointers at the lane's first row
+// and column of the tile, from which every run is a number of rows and columns away
+// that all lanes share, so that a run's address costs the vector unit one addition.
+struct Places {
+  const char* res;
+  char *y, *z, *s;          // y: of the 8-bit result too; s: its scale bytes
+  int m, n;                 // of the first run
+};
+__device__ __forceinline__ long long bytes_away(int rows, int cols, long long ld, int es) {
+  return ((long long)rows * ld + cols) * es;
+}
+// COUNT runs of eight columns of the epilogue, `rows` and `cols` away from the lane's
+// first, from the sums v to the results; nothing is rounded on the way but for the z
+// that is kept.  Each step is done for all runs, so that its branches (the same for
+// all lanes) stand around independent work.  FULL: no row or column lies past the
+// last one.
 template <bool FULL, bool STRM, typename Y, int R, int COUNT>
-__device__ __forceinline__ void epilogue_runs(const Linear8Args& g, const int (&m)[COUNT], int n,
+__device__ __forceinline__ void epilogue_runs(const Linear8Args& g, const Places& at,
+                                              const int (&rows)[COUNT], int cols,
                                               const float (&bias)[8],
                                               const RawRes<R> (&res)[COUNT],
                                               float (&v)[COUNT][8]) {
-  const int left = g.n - n;
+  using Z = KeptOf<Y>;
+  const int left = g.n - at.n - cols;
   // for an 8-bit result a run past the last column pads the last block
-  const bool cols = FULL || (is8<Y> ? n < g.ld_y8 : left > 0);
+  auto in = [&](int s) {
+    return FULL || ((is8<Y> ? at.n + cols < g.ld_y8 : left > 0) && at.m + rows[s] < g.m);
+  };
 #pragma unroll
   for (int s = 0; s < COUNT; ++s)
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[s][e] += bias[e];
   if (g.z) {
-    auto* z = static_cast<KeptOf<Y>*>(g.z) + n;
 #pragma unroll
     for (int s = 0; s < COUNT; ++s)
-      if (FULL || (cols && m[s] < g.m)) store_run<FULL, STRM>(z + (long long)m[s] * g.ldz, left, v[s]);
+      if (in(s))
+        store_run<FULL, STRM>(
+            reinterpret_cast<Z*>(at.z + bytes_away(rows[s], cols, g.ldz, sizeof(Z))), left, v[s]);
   }
   activate(v, g.act);
   if (R != RES_NONE && g.res) {
@@ -117,16 +131,19 @@ __device__ __forceinline__ void epilogue_runs(const Linear8Args& g, const int (&
         for (int e = 0; e < 8; ++e) v[s][e] = e < left ? v[s][e] : 0.f;
       }
       const int byte = block_units(v[s], v[s]);
-      if (FULL || (cols && m[s] < g.m)) {
-        *reinterpret_cast<u32x2_t*>(g.y8 + (long long)m[s] * g.ld_y8 + n) = to_e4m3(v[s]);
-        if ((n & 127) == 0) put_scale(g, m[s], n >> 7, byte);
+      if (in(s)) {
+        *reinterpret_cast<u32x2_t*>(at.y + bytes_away(rows[s], cols, g.ld_y8, 1)) = to_e4m3(v[s]);
+        if (((at.n + cols) & 127) == 0)
+          *reinterpret_cast<unsigned char*>(at.s + bytes_away(rows[s], cols >> 7, g.sld_y8, 1)) =
+              (unsigned char)byte;
       }
     }
   } else {
-    Y* y = static_cast<Y*>(g.y) + n;
 #pragma unroll
     for (int s = 0; s < COUNT; ++s)
-      if (FULL || (cols && m[s] < g.m)) store_run<FULL, STRM>(y + (long long)m[s] * g.ldy, left, v[s]);
+      if (in(s))
+        store_run<FULL, STRM>(
+            reinterpret_cast<Y*>(at.y + bytes_away(rows[s], cols, g.ldy, sizeof(Y))), left, v[s]);
   }
 }
 // The same for four columns; any of them may lie past the last one.
@@ -436,6 +453,14 @@ matmul8_tile_kernel(ProductArgs<EPI> g) {
     for (int i = tid; i < BN; i += 64 * NW)
       Cb[i] = g.bias && n0 + i < g.n ? g.bias[n0 + i] : 0.f;
     __syncthreads();
+    Places at;
+    at.m = m0 + wm * WTM + row_of(0);
+    at.n = n_part + c_run;
+    at.res = static_cast<const char*>(g.res) + bytes_away(at.m, at.n, g.ldr, g.res_fp32 ? 4 : 2);
+    at.z = static_cast<char*>(g.z) + bytes_away(at.m, at.n, g.ldz, sizeof(KeptOf<Y>));
+    at.y = is8<Y> ? reinterpret_cast<char*>(g.y8) + bytes_away(at.m, at.n, g.ld_y8, 1)
+                  : static_cast<char*>(g.y) + bytes_away(at.m, at.n, g.ldy, sizeof(Y));
+    at.s = reinterpret_cast<char*>(g.s8) + bytes_away(at.m, at.n >> 7, g.sld_y8, 1);
     // One copy of the code for all parts: only the staging names accumulators.
     constexpr int COUNT = 2, STEPS = FM * HALVES * RUNS / COUNT;
     static_assert(RUNS % COUNT == 0 && STEPS % 2 == 0, "pairs of steps");
@@ -447,20 +472,23 @@ matmul8_tile_kernel(ProductArgs<EPI> g) {
       // used, in one of two sets of registers: a copy from one to the other would wait
       // for it, and for the stores of the step before.
       RawRes<R> even[COUNT], odd[COUNT];
+      // run s of part p: rows and columns from the lane's first run on
+      auto rows_of = [&](int p, int s) { return p / HALVES * 32 + s * WPG * (64 / RPR); };
       auto fetch = [&](int t, RawRes<R>(&res)[COUNT]) __attribute__((always_inline)) {
-        const int p = t / RUNS, n = n_part + p % HALVES * HC + c_run;
+        const int p = t / RUNS, cols = p % HALVES * HC;
 #pragma unroll
         for (int s = 0; s < COUNT; ++s) {
-          const int m = m0 + wm * WTM + p / HALVES * 32 + row_of(t % RUNS + s);
-          if (FULL || (m < g.m && n < g.n)) res[s].load(g, (long long)m * g.ldr + n, FULL ? 8 : g.n - n);
+          const int rows = rows_of(p, t % RUNS + s);
+          if (FULL || (at.m + rows < g.m && at.n + cols < g.n))
+            res[s].load(at.res + bytes_away(rows, cols, g.ldr, g.res_fp32 ? 4 : 2), g.res_fp32,
+                        FULL ? 8 : g.n - at.n - cols);
         }
       };
       auto step = [&](int t, RawRes<R>(&res)[COUNT]) __attribute__((always_inline)) {
-        const int p = t / RUNS, b = t % RUNS;
-        const int n = n_part + p % HALVES * HC + c_run;
+        const int p = t / RUNS, b = t % RUNS, cols = p % HALVES * HC;
         if (R == RES_ANY && g.res) fetch(t, res);
         float bias[8];
-        const f32x4_t* bl = reinterpret_cast<const f32x4_t*>(Cb + (n - n0));
+        const f32x4_t* bl = reinterpret_cast<const f32x4_t*>(Cb + (at.n + cols - n0));
 #pragma unroll
         for (int e = 0; e < 8; ++e) bias[e] = bl[e / 4][e % 4];
         if (b == 0) {
@@ -469,14 +497,14 @@ matmul8_tile_kernel(ProductArgs<EPI> g) {
             if (p == q) stage(decltype(q)::value / HALVES, decltype(q)::value % HALVES);
           });
         }
-        int m[COUNT];
+        int rows[COUNT];
         float v[COUNT][8];
 #pragma unroll
         for (int s = 0; s < COUNT; ++s) {
-          m[s] = m0 + wm * WTM + p / HALVES * 32 + row_of(b + s);
+          rows[s] = rows_of(p, b + s);
           take(b + s, v[s]);
         }
-        epilogue_runs<FULL, STRM, Y, R>(g, m, n, bias, res, v);
+        epilogue_runs<FULL, STRM, Y, R>(g, at, rows, cols, bias, res, v);
       };
       if constexpr (AHEAD) {
         fetch(0, even);
@@ -502,6 +530,11 @@ matmul8_tile_kernel(ProductArgs<EPI> g) {
       finish(Whole{}, std::integral_constant<int, RES_FP32>{});
     else
       finish(Whole{}, std::integral_constant<int, RES_BF16>{});
+    // the rows of scales, by the workgroups that have the last block
+    if constexpr (is8<Y>) {
+      if (n0 < g.ld_y8 && n0 + BN >= g.ld_y8 && g.sld_y8 > g.ld_y8 >> 7 && tid < BM && m0 + tid < g.m)
+        pad_scales(g, m0 + tid);
+    }
   }
 }
 
@@ -622,7 +655,10 @@ __global__ __launch_bounds__(64 * kFewWaves) void matmul8_rows_kernel(ProductArg
         float q[8] = {v[f][0], v[f][1], v[f][2], v[f][3], 0.f, 0.f, 0.f, 0.f};
         to_units(q, byte, q);
         *reinterpret_cast<unsigned*>(g.y8 + (long long)m * g.ld_y8 + c) = to_e4m3(q)[0];
-        if (wave == 0 && grp == 0) put_scale(g, m, n0 >> 7, byte);
+        if (wave == 0 && grp == 0) {
+          g.s8[(long long)m * g.sld_y8 + (n0 >> 7)] = (unsigned char)byte;
+          if (n0 + 128 >= g.ld_y8) pad_scales(g, m);
+        }
       }
     }
   } else {

@@ -15,7 +15,7 @@ constexpr int kClipTensors = 128;
 // last one ragged.
 constexpr int kClipTile = 16384;
 // Workgroups of a launch at most, each with one partial sum.
-constexpr int kClipGroups = 1024;
+constexpr int kClipGroups = 2048;
 
 struct ClipTable {
   const void* in[kClipTensors];

@@ -11,7 +11,7 @@ import muon_newton_schulz_step_amd as mn
 P = 0x100000  # aligned, never dereferenced by rejected calls
 INVALID, WORKSPACE = mn.MUON_ERR_INVALID_ARG, mn.MUON_ERR_WORKSPACE
 BF16, FP32 = mn.MUON_BF16, mn.MUON_FP32
-TILE, GROUPS, TENSORS = 16384, 1024, 128
+TILE, GROUPS, TENSORS = 16384, 2048, 128
 
 
 def arr(ctype, v):

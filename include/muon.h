@@ -305,7 +305,7 @@ int muon_matmul8(const muon_tensor8* a, const muon_tensor8* b, void* y, int y_dt
                  long long ldy, hipStream_t stream);
 
 /* Activations of a linear layer.  GELU is z Phi(z) with the normal distribution
- * function (within 0.75e-7 of it), GELU_TANH its tanh form; RELU2 is
+ * function (within 2.6e-7 of it), GELU_TANH its tanh form; RELU2 is
  * max(z, 0)^2.  RELU's slope at 0 is 0. */
 typedef enum {
   MUON_ACT_NONE = 0,
@@ -325,8 +325,9 @@ typedef enum {
  *               8-bit result; NULL: not kept.
  *   y or y8     exactly one: bf16 or fp32, or (y NULL) an 8-bit tensor with
  *               1-row blocks, the operand of the next product.
- * Sums are those of muon_matmul8; an 8-bit result's are those of a bf16 one of
- * more than 32 rows, and exact up to 32. */
+ * Sums are those of muon_matmul8.  An 8-bit result's products are exact for sums
+ * of up to 512 columns, of up to 1280 for at most 512 rows, and for at most 32
+ * rows; otherwise they are those of a bf16 result. */
 int muon_linear8(const muon_tensor8* a, const muon_tensor8* b, const float* bias, int activation,
                  const void* residual, int residual_dtype, long long ldr, void* z, long long ldz,
                  void* y, int y_dtype, long long ldy, const muon_tensor8* y8, hipStream_t stream);

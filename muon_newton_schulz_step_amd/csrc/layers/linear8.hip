@@ -8,10 +8,16 @@ namespace {
 constexpr int kOut8 = 2;
 
 // Whether an 8-bit result comes from exact products.  Rounding to 8 bits turns an
-// error of relative size e into flips of a whole step for a share e / 2^-4 of the
-// values, sqrt(e 2^-4) in the norm.  The 8-bit instruction's cut leaves e near
-// 1e-4 where a few columns of a are 64 times the others.  XXX
-bool exact8(int m, int ld) { return ld <= 512 || m <= 512; }
+// error of relative size e into flips of a whole step, 2^-4, for a share e / 2^-4 of the
+// values: sqrt(e 2^-4) in the norm.  The 8-bit instruction's cut leaves e near 1e-4
+// where a few columns of a are 64 times the others, and more where the sum is short
+// and few of them share it: an MLP's result (squared ReLU, those columns 1% of all) was
+// off by 6.2e-3 of its norm for 200 rows of 128, 5.6e-3 for 60 of 520, 3 to 3.7e-3 for
+// thousands of rows and 520 or more columns; with exact products by 1.7e-3, what its
+// rounding to bf16 does.  Exact costs 99 us against 74 (8192 x 8192 x 512), 26 against
+// 20 (8192 x 2048 x 512), 14 against 12 (512 x 5120 x 1280), but 62 against 35 at 512 x
+// 16384 x 4096.
+bool exact8(int m, int ld) { return ld <= 512 || (m <= 512 && ld <= 1280); }
 
 template <int BM, int BN, int WGM, int WGN, bool EXACT, typename Y>
 void tiles(Linear8Args a, hipStream_t s) {

@@ -461,7 +461,10 @@ matmul8_tile_kernel(ProductArgs<EPI> g) {
     at.y = is8<Y> ? reinterpret_cast<char*>(g.y8) + bytes_away(at.m, at.n, g.ld_y8, 1)
                   : static_cast<char*>(g.y) + bytes_away(at.m, at.n, g.ldy, sizeof(Y));
     at.s = reinterpret_cast<char*>(g.s8) + bytes_away(at.m, at.n >> 7, g.sld_y8, 1);
-    // One copy of the code for all parts: only the staging names accumulators.
+    // One copy of the code for all parts (only the staging names accumulators), but for
+    // whole tiles without a residual, whose steps are written out: 2% of a product of
+    // 16384 x 16384 x 4096 to 8 bits.  With everything written out the compiler spills
+    // hundreds of registers.
     constexpr int COUNT = 2, STEPS = FM * HALVES * RUNS / COUNT;
     static_assert(RUNS % COUNT == 0 && STEPS % 2 == 0, "pairs of steps");
     auto finish = [&](auto full, auto res_kind) __attribute__((always_inline)) {
@@ -516,6 +519,8 @@ matmul8_tile_kernel(ProductArgs<EPI> g) {
           fetch(t + 2 * COUNT < STEPS * COUNT ? t + 2 * COUNT : 0, even);
           step(t + COUNT, odd);
         }
+      } else if constexpr (FULL) {
+        static_for<STEPS>([&](auto t) { step(decltype(t)::value * COUNT, even); });
       } else {
 #pragma unroll 1
         for (int t = 0; t < STEPS * COUNT; t += COUNT) step(t, even);

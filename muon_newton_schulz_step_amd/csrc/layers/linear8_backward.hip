@@ -12,10 +12,7 @@
 
 namespace muon {
 
-namespace {
 constexpr int kBackWaves = 8;
-constexpr int kBackRows = 4;  // rows of a wave that are on their way together
-}  // namespace
 
 template <typename D, typename Z>
 __global__ __launch_bounds__(64 * kBackWaves) void linear8_back_kernel(Linear8BackArgs a) {
@@ -23,46 +20,29 @@ __global__ __launch_bounds__(64 * kBackWaves) void linear8_back_kernel(Linear8Ba
   const int piece = blockIdx.x, c = piece * 512 + lane * 8;
   const long long step = (long long)gridDim.y * kBackWaves;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (long long first = (long long)blockIdx.y * kBackWaves + wave; first < a.rows;
-       first += step * kBackRows) {
-    Raw8<D> rd[kBackRows];
-    Raw8<Z> rz[kBackRows];
+  Raw8<D> rd;
+  Raw8<Z> rz;
+  auto fetch = [&](long long row) __attribute__((always_inline)) {
+    rd.load(static_cast<const D*>(a.dy) + row * a.lddy + c, a.cols - c);
+    if (a.act != MUON_ACT_NONE)
+      rz.load(static_cast<const Z*>(a.z) + row * a.ldz + c, a.cols - c);
+  };
+  long long row = (long long)blockIdx.y * kBackWaves + wave;
+  if (row < a.rows) fetch(row);
+  for (; row < a.rows; row += step) {
+    float d[8], z[8];
+    rd.get(d);
+    if (a.act != MUON_ACT_NONE) rz.get(z);
+    if (row + step < a.rows) fetch(row + step);
+    if (a.act != MUON_ACT_NONE) activate_grad(d, z, a.act);
 #pragma unroll
-    for (int k = 0; k < kBackRows; ++k) {
-      const long long row = first + k * step;
-      if (row < a.rows) {
-        rd[k].load(static_cast<const D*>(a.dy) + row * a.lddy + c, a.cols - c);
-        if (a.act != MUON_ACT_NONE)
-          rz[k].load(static_cast<const Z*>(a.z) + row * a.ldz + c, a.cols - c);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kBackRows; ++k) {
-      const long long row = first + k * step;
-      if (row >= a.rows) break;
-      float d[8];
-      rd[k].get(d);
-      if (a.act != MUON_ACT_NONE) {
-        float z[8];
-        rz[k].get(z);
-        activate_grad(d, z, a.act);
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum[i] += d[i];
-      if (a.dz) store8_edge(static_cast<bf16_t*>(a.dz) + row * a.lddz + c, a.cols - c, d);
-      if (a.q) {
-        unsigned top = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const unsigned f = finite_bits(d[i]);
-          top = top > f ? top : f;
-        }
-        const int byte = scale_byte(max16(top));
-        to_units(d, byte, d);
-        if (c < a.ld) *reinterpret_cast<u32x2_t*>(a.q + row * a.ld + c) = to_e4m3(d);
-        const unsigned word = pack_scales(byte);
-        if (lane == 0) *reinterpret_cast<unsigned*>(a.s + row * a.sld + 4 * piece) = word;
-      }
+    for (int i = 0; i < 8; ++i) sum[i] += d[i];
+    if (a.dz) store8_edge(static_cast<bf16_t*>(a.dz) + row * a.lddz + c, a.cols - c, d);
+    if (a.q) {
+      const int byte = block_units(d, d);
+      if (c < a.ld) *reinterpret_cast<u32x2_t*>(a.q + row * a.ld + c) = to_e4m3(d);
+      const unsigned word = pack_scales(byte);
+      if (lane == 0) *reinterpret_cast<unsigned*>(a.s + row * a.sld + 4 * piece) = word;
     }
   }
   if (!a.dbias) return;
@@ -105,12 +85,14 @@ __global__ __launch_bounds__(1024) void bias_reduce_kernel(const float* part, in
   }
 }
 
-// Workgroups along the rows: 1024 in all, each wave with at least two rows.
+// Workgroups along the rows: at most 512 in all, which the chip holds at once, as few
+// as give no wave more rows than that many would, and at least two rows to a wave.
 int linear8_back_groups(int rows, int cols) {
   const long long strips = (cols + 511LL) / 512;
-  const long long most = strips < 1024 ? 1024 / strips : 1;
-  const long long fit = ((long long)rows + 2 * kBackWaves - 1) / (2 * kBackWaves);
-  return (int)(fit < most ? fit : most);
+  const long long most = strips < 512 ? 512 / strips : 1;
+  const long long all = ((long long)rows + kBackWaves - 1) / kBackWaves;  // rows of a wave
+  const long long each = (all + most - 1) / most;
+  return (int)((all + (each < 2 ? 2 : each) - 1) / (each < 2 ? 2 : each));
 }
 
 hipError_t launch_linear8_backward(int dy_fp32, int z_fp32, const Linear8BackArgs& a,

@@ -599,9 +599,12 @@ void with_shape(int cols, bool branch, F&& f) {
   }
 #undef MUON_SHAPE
 }
+// Workgroups for `rows` rows, `teams` to a workgroup, at most `most`, which are what the
+// chip holds at once: as few as give none of them more rows than that many would.
 int groups_for(int rows, int teams, int most) {
-  const long long g = ((long long)rows + teams - 1) / teams;
-  return (int)(g < most ? g : most);
+  const long long all = ((long long)rows + teams - 1) / teams;  // rows of a team
+  const long long each = (all + most - 1) / most;
+  return each > 0 ? (int)((all + each - 1) / each) : 0;
 }
 using Bf16 = std::integral_constant<int, MUON_BF16>;
 using Fp32 = std::integral_constant<int, MUON_FP32>;
@@ -628,7 +631,8 @@ hipError_t launch_residual_norm(int x_bf16, int b_bf16, const ResidualArgs& a, h
     with_shape<false>(a.cols, false, [&](auto team, auto nch) {
       constexpr int T = decltype(team)::value, N = decltype(nch)::value;
       constexpr int waves = forward_waves(T);
-      const dim3 grid(groups_for(a.rows, waves / T, 8192 / waves)), block(64 * waves);
+      // 16 waves to a CU
+      const dim3 grid(groups_for(a.rows, waves / T, 256 * (16 / waves))), block(64 * waves);
       hipLaunchKernelGGL((residual_norm_kernel<decltype(xt)::value, decltype(bt)::value, T, N>), grid,
                          block, 0, s, a);
     });

@@ -79,7 +79,7 @@ def test_backward_refusals(kw, expect):
 def test_workspace_sizes():
     f = mn.linear8_backward_workspace_bytes
     assert f(16, 5120) == 0 and f(17, 512) == 2 * 512 * 4      # two rows to a wave of eight
-    assert f(1 << 20, 512) == 1024 * 512 * 4 and f(1 << 20, 1 << 22) == 0
+    assert f(1 << 20, 512) == 512 * 512 * 4 and f(1 << 20, 1 << 22) == 0
     assert f(0, 8) == f(-1, 8) == f(8, 0) == f(8, (1 << 22) + 1) == f(1 << 40, 8) == 0
 
 

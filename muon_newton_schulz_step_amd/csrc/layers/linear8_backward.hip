@@ -1,7 +1,10 @@
 // The backward pass of linear8 up to its two gradient products:
 //   dz = dy act'(z)  in bf16 and, with a scale per block of 1 x 128, in 8 bits,
 //   dbias = sum over the rows of dz.
-// One pass over dy and z, bound by HBM.
+// One pass over dy and z, bound by HBM: 8192 x 5120 squared ReLU 51.5 us with the
+// reduction (5.7 TB/s, some of it from the last-level cache), 60 + 5 us traced with
+// cold inputs; GELU 58 us.  A wave has one row in work and one on its way: two or four
+// at a time took 54.5 and 59.6 us.
 //
 // A workgroup of 8 waves has a strip of 512 columns, 8 to a lane, as the
 // conversion to 8 bits does (16 lanes hold a block), and a share of the rows: the

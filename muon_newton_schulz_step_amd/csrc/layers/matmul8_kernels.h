@@ -19,7 +19,10 @@
 //   tiles   both operands through LDS, for many rows of a: bound by the MFMAs;
 //   rows    few rows of a (up to 32): bound by reading b once, so always exact.
 // Both with an epilogue too (EPI, for linear8): z = y + bias, kept where it is
-// asked for, and act(z) + residual in bf16, fp32 or 8 bits.
+// asked for, and act(z) + residual in bf16, fp32 or 8 bits.  What that costs a product
+// of 16384 x 16384 x 4096 (815 us on the same card): bias 15 us, squared ReLU 20, GELU
+// 110, a bf16 residual 90 (512 MB), an 8-bit result 58, and all of GELU, z kept and 8
+// bits 180; one of 4096 x 5120 x 1280 (38 us): 1, 2, 5, 6, 2 and 11.
 #pragma once
 
 #include "muon_gemm.h"

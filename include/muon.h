@@ -454,7 +454,9 @@ typedef struct {
  *   branch      as there; read only where params has post_weight or gate, may be
  *               NULL otherwise.
  *   x           as there; read only for the scale's gradient, may be NULL otherwise.
- *   grads       those of parameters that params does not have must be NULL;
+ *   params      its bias and eps are not read (grads->bias may be asked for with
+ *               bias NULL).
+ *   grads       those of other parameters that params does not have must be NULL;
  *               added to with accumulate.
  *   workspace   muon_residual_norm_backward_workspace_bytes for these sizes
  *               (`branch_params` 1 where params has post_weight or gate, else 0). */

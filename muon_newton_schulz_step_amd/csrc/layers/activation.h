@@ -29,10 +29,12 @@ __device__ __forceinline__ float normal_tail(float z, float& density) {
   density = exp2_fast(-0.72134752f * (z * z));
   return p * t * density;
 }
-// z Phi(z): for z > 0 z - z tail, else z tail
+// z Phi(z): for z > 0 z - z tail, else z tail.  Beyond 30 the tail is zero, which an
+// infinity must not meet as a factor.
 __device__ __forceinline__ float gelu(float z) {
   float e;
-  return fmaf(-fabsf(z), normal_tail(z, e), __builtin_fmaxf(z, 0.f));
+  const float tail = normal_tail(z, e);
+  return fmaf(-__builtin_fminf(fabsf(z), 30.f), tail, __builtin_fmaxf(z, 0.f));
 }
 
 // (a NaN is below nothing and stays one)

@@ -327,7 +327,8 @@ def linear8(a, b, bias=None, *, activation=None, residual=None, keep: bool = Fal
     1 x 128, the next product's operand.  ``bias`` is fp32, ``residual`` bf16 or fp32;
     ``activation`` None, "relu", "relu2" (squared), "gelu", "gelu_tanh" or
     "silu".  ``keep`` returns (y, z) with z = a b^T + bias for linear8_backward, in
-    y's dtype (bf16 beside a Tensor8).  ``out`` (bf16 or fp32) may have a row stride.
+    y's dtype (bf16 beside a Tensor8).  ``out`` may be given: a matrix in bf16 or fp32,
+    which may have a row stride, or a Tensor8.
     Everything is fp32 up to the one rounding of each result; the sums are those
     of matmul8."""
     torch = _T or _torch()
@@ -347,11 +348,14 @@ def linear8(a, b, bias=None, *, activation=None, residual=None, keep: bool = Fal
         rcode = _dtype_code(residual.dtype)
         if n:
             rp, _, _, ldr = _matrix(residual, "residual")
-    out8 = out is None and out_dtype == torch.float8_e4m3fn
-    if out8 and n == 0:
-        raise ValueError("an 8-bit result has at least one column")
+    out8 = isinstance(out, Tensor8) or (out is None and out_dtype == torch.float8_e4m3fn)
     if out8:
-        out = Tensor8.empty(m, n, 1, device)
+        if n == 0:
+            raise ValueError("an 8-bit result has at least one column")
+        if out is None:
+            out = Tensor8.empty(m, n, 1, device)
+        elif out.shape != (m, n) or out.block_rows != 1 or out_dtype not in (None, torch.float8_e4m3fn):
+            raise ValueError("out must be (a.rows, b.rows), with blocks of 1 x 128, and of out_dtype")
         yp, code, ldy, y8 = None, MUON_BF16, n, out._c
     elif out is None:
         out = torch.empty(m, n, dtype=out_dtype or torch.bfloat16, device=device)

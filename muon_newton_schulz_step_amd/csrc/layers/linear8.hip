@@ -54,7 +54,18 @@ void go(const Linear8Args& a, const Matmul8Plan& p, hipStream_t s) {
         hipLaunchKernelGGL((matmul8_rows_kernel<2, 2, Y, true>), grid, block, 0, s, a);
     }
   } else if (p.bm == 64) {
-    if constexpr (!is8<Y>) tiles<64, 64, 2, 1, FP32, Y>(a, s);
+    if (p.bn == 128) {
+      if constexpr (is8<Y>) {
+        if (exact8(a.m, a.ld))
+          tiles<64, 128, 2, 2, true, Y>(a, s);
+        else
+          tiles<64, 128, 2, 2, false, Y>(a, s);
+      } else if constexpr (FP32) {
+        tiles<64, 128, 2, 2, true, Y>(a, s);
+      }
+    } else if constexpr (!is8<Y>) {
+      tiles<64, 64, 2, 1, FP32, Y>(a, s);
+    }
   } else if (is8<Y> && exact8(a.m, a.ld)) {
     if constexpr (is8<Y>) {
       if (p.bm == 128)
@@ -70,19 +81,40 @@ void go(const Linear8Args& a, const Matmul8Plan& p, hipStream_t s) {
 }
 }  // namespace
 
+// The tile by the time of the fullest CU per k-tile, in us, as for the plain product,
+// with one of 64 x 128 beside the others for results in fp32 and 8 bits: of those a CU
+// holds three, which fill the last round of a middle-sized grid better.  Measured at
+// 100 to 16384 rows, 768 to 5120 columns and sums of 700 to 5120 (in us; fp32 with a
+// residual, 8 bits with z kept):
+//   fp32    4099 x 1280 x 5120 65.4 -> 57.7, 1027 x 5120 x 1280 25.2 -> 21.4, 300 x 4096
+//           x 4096 27.2 -> 22.5; but 16384 x 1280 x 5120 184 against 193
+//   8 bits  600 x 1280 x 5120 33.3 -> 26.5, 4099 x 768 x 3080 23.6 -> 20.2; but 2048 x
+//           4096 x 4096 35.4 against 52.6
+// In bf16 it gains at few sizes (4099 x 768 x 3080 21.8 -> 18.7) and is not taken.
 Matmul8Plan linear8_plan(int out, int m, int n, int ld) {
-  if (out != kOut8) return matmul8_plan(out == MUON_BF16, m, n, ld);
+  auto share = [&](int bm, int bn) {  // tiles of the fullest CU
+    return (double)(((long long)((m + bm - 1) / bm) * ((n + bn - 1) / bn) + 255) / 256);
+  };
+  const double q64 = share(64, 64), q96 = share(64, 128), q128 = share(128, 128);
+  const double odd = (long long)q128 % 2 ? 1.0 : 0.0;
+  // exact products
+  const double e64 = 0.2 + 0.25 * q64, e96 = 0.08 + 0.44 * q96;
+  const double e128 = (q128 <= 2 ? 0.77 : 0.87) * q128;
+  if (out != kOut8) {
+    const Matmul8Plan p = matmul8_plan(out == MUON_BF16, m, n, ld);
+    if (out == MUON_FP32 && !p.few && p.bm <= 128 && e96 < (p.bm == 64 ? e64 : e128))
+      return {false, 64, 128};
+    return p;
+  }
   // An 8-bit result needs whole blocks of 128 columns in a workgroup.
   if (m <= 32) return {true, m <= 16 ? 16 : 32, 128};
-  // the costs of the plain product's tiles
-  auto share = [&](int b) {
-    return (double)(((long long)((m + b - 1) / b) * ((n + b - 1) / b) + 255) / 256);
-  };
-  const double q128 = share(128), q256 = share(256), odd = (long long)q128 % 2 ? 1.0 : 0.0;
-  const bool small = exact8(m, ld) ? 0.9 * q128 + 0.2 * odd < 3.3 * q256
-                                : 0.44 * q128 + 0.28 * odd < 1.55 * q256;
-  const int b = small ? 128 : 256;
-  return {false, b, b};
+  const double q256 = share(256, 256);
+  const bool exact = exact8(m, ld);
+  const double t96 = exact ? e96 : 0.1 + 0.3 * q96;
+  const double t128 = exact ? e128 : 0.44 * q128 + 0.28 * odd;
+  const double t256 = exact ? 3.3 * q256 : 1.55 * q256;
+  if (t96 < t128 && t96 < t256) return {false, 64, 128};
+  return t128 < t256 ? Matmul8Plan{false, 128, 128} : Matmul8Plan{false, 256, 256};
 }
 
 hipError_t launch_linear8(int out, const Linear8Args& a, const Matmul8Plan& p, hipStream_t s) {

@@ -211,9 +211,10 @@ matmul8_tile_kernel(ProductArgs<EPI> g) {
   // and of 64 scale words per four; where there are more waves than those, the
   // others load the same again
   constexpr int SG = (BM + BN) / 64, SPW = SG > NW ? SG / NW : 1;
-  static_assert(DPW * 64 * NW == STAGE && B_CHUNKS % (DPW * 64) == 0, "one operand per wave");
-  static_assert((SG % NW == 0 || NW % SG == 0) && BN % (SPW * 64) == 0,
-                "one operand's scales per wave");
+  // a wave's loads are of one operand, or (MIXED) each is of one, told by its place
+  constexpr bool MIXED = B_CHUNKS % (DPW * 64) != 0;
+  static_assert(DPW * 64 * NW == STAGE && B_CHUNKS % 64 == 0, "whole loads");
+  static_assert((SG % NW == 0 || SG < NW) && BN % (SPW * 64) == 0, "one operand's scales per wave");
   static_assert(FN % 2 == 0, "halves of a wave's columns are staged");
   __shared__ u32x4_t S0[STAGE], S1[STAGE];
   __shared__ __attribute__((aligned(16))) unsigned C0[BM + BN];
@@ -229,21 +230,32 @@ matmul8_tile_kernel(ProductArgs<EPI> g) {
   const int m0 = (first + idx % gm) * BM, n0 = (idx / gm) * BN;
 
   const int wave_s = __builtin_amdgcn_readfirstlane(wave);
-  const bool is_b = wave_s * DPW * 64 < B_CHUNKS;
-  const unsigned char* base = is_b ? g.b + (long long)n0 * g.ld : g.a + (long long)m0 * g.ld;
-  const int last_row = is_b ? g.n - 1 - n0 : g.m - 1 - m0;
+  auto of_b = [&](int d) { return (wave_s * DPW + (MIXED ? d : 0)) * 64 < B_CHUNKS; };
+  auto base_of = [&](int d) __attribute__((always_inline)) {
+    return of_b(d) ? g.b + (long long)n0 * g.ld : g.a + (long long)m0 * g.ld;
+  };
+  const unsigned char* base = base_of(0);
   unsigned voff[DPW];
 #pragma unroll
   for (int d = 0; d < DPW; ++d) {
+    const bool is_b = of_b(d);
+    const int last_row = is_b ? g.n - 1 - n0 : g.m - 1 - m0;
     const int q = (wave * DPW + d) * 64 + lane;
     const int r = q / CPR, rl = is_b ? r : r - BN;
     voff[d] = (unsigned)(rl < last_row ? rl : last_row) * (unsigned)g.ld + swz(q % CPR, r) * 16;
   }
   const int nk = g.ld / 128, last_word = (nk - 1) / 4;
   auto issue = [&](int kt, u32x4_t* St) __attribute__((always_inline)) {
-    const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(base + (long long)kt * 128);
+    if constexpr (MIXED) {
 #pragma unroll
-    for (int d = 0; d < DPW; ++d) buffer_load_lds16(rs, voff[d], St + (wave_s * DPW + d) * 64);
+      for (int d = 0; d < DPW; ++d)
+        buffer_load_lds16(buffer_rsrc(base_of(d) + (long long)kt * 128), voff[d],
+                          St + (wave_s * DPW + d) * 64);
+    } else {
+      const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(base + (long long)kt * 128);
+#pragma unroll
+      for (int d = 0; d < DPW; ++d) buffer_load_lds16(rs, voff[d], St + (wave_s * DPW + d) * 64);
+    }
   };
   // word w of the scales of the tile's rows: b's, then a's
   const int sg = SG < NW ? wave_s % SG : wave_s * SPW;

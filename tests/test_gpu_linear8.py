@@ -71,7 +71,28 @@ def rounded(x, dtype):
 # three tiles, ragged in each direction, a k shorter than a block, several blocks
 SIZES = [(1, 1, 1), (1, 130, 384), (3, 257, 129), (16, 5120, 256), (17, 640, 130), (32, 8200, 128),
          (33, 129, 515), (70, 1003, 640), (129, 384, 1), (300, 1300, 257), (513, 8000, 130),
-         (2100, 2050, 140), (4099, 4000, 64)]
+         (2100, 2050, 140), (4099, 4000, 64), (1027, 5120, 130), (1030, 640, 530), (2048, 4096, 64), (2100, 2050, 600)]
+
+
+@pytest.mark.parametrize("m,n,k,out,bm,bn", [
+    (1027, 5120, 130, FP32, 64, 128), (1030, 640, 530, E4M3, 64, 128), (300, 1300, 257, E4M3, 64, 128),
+    (2048, 4096, 64, E4M3, 128, 128), (2100, 2050, 600, E4M3, 128, 128), (2560, 4097, 600, E4M3, 256, 256),
+    (8192, 4096, 64, E4M3, 256, 256), (2100, 2050, 140, BF16, 128, 128), (2560, 4097, 600, BF16, 256, 256),
+    (70, 1003, 640, FP32, 64, 64), (2048, 4096, 64, FP32, 128, 128), (8192, 4096, 64, FP32, 256, 256)])
+def test_tiles(m, n, k, out, bm, bn):
+    """The sizes of these tests reach the tiles: read from the flops that a launch executes."""
+    announce("linear8 tile", m, n, k, out)
+    a, b = mn.quantize8(whole(m, k, seed=m), 1), mn.quantize8(whole(n, k, seed=n + 1), 128)
+    mn.timing_read()
+    mn.timing_enable(True)
+    try:
+        mn.linear8(a, b, out_dtype=out)
+        torch.cuda.synchronize()
+        (r,) = mn.timing_read()
+    finally:
+        mn.timing_enable(False)
+    pad = lambda v, t: -(-v // t) * t  # noqa: E731
+    assert r["kind"] == "linear8" and r["exec_flops"] == 2.0 * pad(m, bm) * pad(n, bn) * pad(k, 128)
 
 
 @pytest.mark.parametrize("out", [BF16, FP32, E4M3])
@@ -94,6 +115,21 @@ def test_whole_numbers(m, n, k, out):
             check8(got, y)
         else:
             assert got.dtype == out and np.array_equal(to64(got), rounded(y, out))
+
+
+@pytest.mark.parametrize("out", [FP32, E4M3])
+def test_whole_numbers_large_exact_tile(out):
+    """256 x 256 tiles of exact products."""
+    announce("linear8 of whole numbers, 256 x 256 exact tiles", out)
+    m, n, k = 8192, 4096, 64
+    a, b = mn.quantize8(whole(m, k, seed=1), 1), mn.quantize8(whole(n, k, seed=2), 128)
+    bias, res = whole(n, seed=3, top=9), whole(m, n, seed=4, top=50, dtype=BF16)
+    y, _ = lo.linear8(values(a), values(b), to64(bias), "relu2", to64(res))
+    got = mn.linear8(a, b, bias, activation="relu2", residual=res, out_dtype=out)
+    if out == E4M3:
+        check8(got, y)
+    else:
+        assert np.array_equal(to64(got), y)
 
 
 def slope_and_error(z, act):
@@ -157,9 +193,11 @@ def test_activations(act, out):
 @pytest.mark.parametrize("out", [BF16, E4M3])
 def test_large_tile(out):
     announce("linear8 256 x 256 tiles", out)
-    check_real(2560, 4097, 300, "gelu", out, BF16)
+    check_real(2560, 4097, 600, "gelu", out, BF16)
     check_real(1027, 260, 1283, "silu", out, None, ba=128, bb=1)
     check_real(300, 260, 1290, "relu2", out, FP32)
+    check_real(1030, 640, 1300, "gelu_tanh", out, BF16)
+    check_real(1027, 5120, 200, "silu", FP32, FP32)
 
 
 def test_strides_and_out():

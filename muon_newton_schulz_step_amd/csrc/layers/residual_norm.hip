@@ -11,7 +11,10 @@
 //   dpw = gate S1,  dpb = gate S0,  dgate = pw S1 + pb S0,
 // so that four sums per column serve five gradients.
 // h comes from r in fp32, before r is rounded to the stream's type.  All sums are
-// fp32, ds fp64 (it has rows x cols terms of either sign).
+// fp32, ds fp64 over pairs in fp32: it has rows x cols terms of either sign, and whole
+// lanes of a row in fp32 were 1.1 to 1.7 times as far off (4096 x 1280 by 1.9 against
+// 1.1 times 2^-24 sqrt(terms)) for 0 to 3% less time (16384 columns -8 to 9%); every term in fp64 would be off by 1.0
+// and cost up to 14% (16384 x 1280 fp32, bf16 branch: 104, 105 and 118 us).
 //
 // Both passes read each element once and are bound by HBM:
 //   16384 x 1280 fp32, bf16 branch, gate and scale, to 8 bits 46 us (5.0 TB/s; a copy
@@ -368,7 +371,6 @@ residual_back_kernel(ResidualBackArgs a) {
     const float mu = st[0], r = st[1], pmu = st[2], pr = post ? st[3] : 1.f;
     float x[NCH][8], d[NCH][8], bh[BRANCH ? NCH : 1][8];
     float c[2] = {0.f, 0.f};
-    float ds = 0.f;
     if (in) {
       static_for<NCH>([&](auto kk) {
         constexpr int k = decltype(kk)::value;
@@ -416,8 +418,8 @@ residual_back_kernel(ResidualBackArgs a) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const float v = fmaf(r, d[k][i] - c0 - x[k][i] * c1, dr[i]);
-          if (a.g.scale) ds = fmaf(v, xs[i], ds);
           d[k][i] = v;
+          if (a.g.scale && i % 2) dscale += (double)fmaf(v, xs[i], d[k][i - 1] * xs[i - 1]);
           if constexpr (BRANCH) {
             const float h = (bh[k][i] - pmu) * pr;
             p[i] = v * h;
@@ -432,7 +434,6 @@ residual_back_kernel(ResidualBackArgs a) {
           add(std::integral_constant<int, 3>{}, kk, d[k]);
         }
       });
-      dscale += (double)ds;
       if (EARLY && row + step < a.rows) {
         fetch(row + step);
         fetch_late(row + step);

@@ -11,10 +11,11 @@
 //   dpw = gate S1,  dpb = gate S0,  dgate = pw S1 + pb S0,
 // so that four sums per column serve five gradients.
 // h comes from r in fp32, before r is rounded to the stream's type.  All sums are
-// fp32, ds fp64 over pairs in fp32: it has rows x cols terms of either sign, and whole
+// fp32, ds fp64 over pairs in fp32: it has rows x cols terms of either sign.  Whole
 // lanes of a row in fp32 were 1.1 to 1.7 times as far off (4096 x 1280 by 1.9 against
-// 1.1 times 2^-24 sqrt(terms)) for 0 to 3% less time (16384 columns -8 to 9%); every term in fp64 would be off by 1.0
-// and cost up to 14% (16384 x 1280 fp32, bf16 branch: 104, 105 and 118 us).
+// 1.1 times 2^-24 sqrt(terms)) for 0 to 3% less time (16384 columns -8 to 9%); with
+// every term in fp64 it is off by 1.0 and costs up to 14% (16384 x 1280 fp32, bf16
+// branch: 104, 105 and 118 us).
 //
 // Both passes read each element once and are bound by HBM:
 //   16384 x 1280 fp32, bf16 branch, gate and scale, to 8 bits 46 us (5.0 TB/s; a copy

@@ -7,7 +7,8 @@ namespace muon {
 namespace {
 constexpr int kOut8 = 2;
 
-// Whether an 8-bit result comes from exact products.  Rounding to 8 bits turns an
+// Whether an 8-bit result comes from exact products where its caller leaves that open
+// (one that asks for them gets them at every size).  Rounding to 8 bits turns an
 // error of relative size e into flips of a whole step, 2^-4, for a share e / 2^-4 of the
 // values: sqrt(e 2^-4) in the norm.  The 8-bit instruction's cut leaves e near 1e-4
 // where a few columns of a are 64 times the others, and more where the sum is short
@@ -16,7 +17,9 @@ constexpr int kOut8 = 2;
 // thousands of rows and 520 or more columns; with exact products by 1.7e-3, what its
 // rounding to bf16 does.  Exact costs 99 us against 74 (8192 x 8192 x 512), 26 against
 // 20 (8192 x 2048 x 512), 14 against 12 (512 x 5120 x 1280), but 62 against 35 at 512 x
-// 16384 x 4096.
+// 16384 x 4096.  By its caller's choice: the up projection of an MLP with z kept 43 ->
+// 58 us (4096 x 5120 x 1280) and 979 -> 1705 (16384 x 16384 x 4096), its result off by
+// 1.7e-3 instead of 3.0e-3 and 2.4e-3.
 bool exact8(int m, int ld) { return ld <= 512 || (m <= 512 && ld <= 1280); }
 
 template <int BM, int BN, int WGM, int WGN, bool EXACT, typename Y>
@@ -35,7 +38,6 @@ void tiles(Linear8Args a, hipStream_t s) {
 
 template <typename Y>
 void go(const Linear8Args& a, const Matmul8Plan& p, hipStream_t s) {
-  constexpr bool FP32 = std::is_same_v<Y, float>;
   if (p.few) {
     const dim3 grid((a.n + p.bn - 1) / p.bn), block(64 * kFewWaves);
     if constexpr (is8<Y>) {
@@ -53,30 +55,24 @@ void go(const Linear8Args& a, const Matmul8Plan& p, hipStream_t s) {
       else
         hipLaunchKernelGGL((matmul8_rows_kernel<2, 2, Y, true>), grid, block, 0, s, a);
     }
-  } else if (p.bm == 64) {
-    if (p.bn == 128) {
-      if constexpr (is8<Y>) {
-        if (exact8(a.m, a.ld))
-          tiles<64, 128, 2, 2, true, Y>(a, s);
-        else
-          tiles<64, 128, 2, 2, false, Y>(a, s);
-      } else if constexpr (FP32) {
-        tiles<64, 128, 2, 2, true, Y>(a, s);
-      }
-    } else if constexpr (!is8<Y>) {
-      tiles<64, 64, 2, 1, FP32, Y>(a, s);
-    }
-  } else if (is8<Y> && exact8(a.m, a.ld)) {
-    if constexpr (is8<Y>) {
-      if (p.bm == 128)
-        tiles<128, 128, 4, 2, true, Y>(a, s);
-      else
-        tiles<256, 256, 4, 2, true, Y>(a, s);
-    }
-  } else if (p.bm == 128) {
-    tiles<128, 128, FP32 ? 4 : 2, 2, FP32, Y>(a, s);
-  } else {
-    tiles<256, 256, 4, 2, FP32, Y>(a, s);
+  } else if (p.exact) {
+    if (p.bm == 64 && p.bn == 128)
+      tiles<64, 128, 2, 2, true, Y>(a, s);
+    else if (p.bm == 128)
+      tiles<128, 128, 4, 2, true, Y>(a, s);
+    else if (p.bm == 256)
+      tiles<256, 256, 4, 2, true, Y>(a, s);
+    else if constexpr (!is8<Y>)
+      tiles<64, 64, 2, 1, true, Y>(a, s);
+  } else if constexpr (!std::is_same_v<Y, float>) {
+    if (p.bm == 128)
+      tiles<128, 128, 2, 2, false, Y>(a, s);
+    else if (p.bm == 256)
+      tiles<256, 256, 4, 2, false, Y>(a, s);
+    else if constexpr (is8<Y>)
+      tiles<64, 128, 2, 2, false, Y>(a, s);
+    else
+      tiles<64, 64, 2, 1, false, Y>(a, s);
   }
 }
 }  // namespace
@@ -90,8 +86,9 @@ void go(const Linear8Args& a, const Matmul8Plan& p, hipStream_t s) {
 //           x 4096 27.2 -> 22.5; but 16384 x 1280 x 5120 184 against 193
 //   8 bits  600 x 1280 x 5120 33.3 -> 26.5, 4099 x 768 x 3080 23.6 -> 20.2; but 2048 x
 //           4096 x 4096 35.4 against 52.6
-// In bf16 it gains at few sizes (4099 x 768 x 3080 21.8 -> 18.7) and is not taken.
-Matmul8Plan linear8_plan(int out, int m, int n, int ld) {
+// In bf16 it gains at few sizes (4099 x 768 x 3080 21.8 -> 18.7) and is not taken, but
+// for exact products, whose costs are those of a result in fp32.
+Matmul8Plan linear8_plan(int out, int m, int n, int ld, bool exact) {
   auto share = [&](int bm, int bn) {  // tiles of the fullest CU
     return (double)(((long long)((m + bm - 1) / bm) * ((n + bn - 1) / bn) + 255) / 256);
   };
@@ -101,20 +98,21 @@ Matmul8Plan linear8_plan(int out, int m, int n, int ld) {
   const double e64 = 0.2 + 0.25 * q64, e96 = 0.08 + 0.44 * q96;
   const double e128 = (q128 <= 2 ? 0.77 : 0.87) * q128;
   if (out != kOut8) {
-    const Matmul8Plan p = matmul8_plan(out == MUON_BF16, m, n, ld);
-    if (out == MUON_FP32 && !p.few && p.bm <= 128 && e96 < (p.bm == 64 ? e64 : e128))
-      return {false, 64, 128};
+    exact = exact || out == MUON_FP32;
+    Matmul8Plan p = matmul8_plan(!exact, m, n, ld);
+    if (exact && !p.few && p.bm <= 128 && e96 < (p.bm == 64 ? e64 : e128)) p = {false, 64, 128};
+    p.exact = exact;
     return p;
   }
   // An 8-bit result needs whole blocks of 128 columns in a workgroup.
   if (m <= 32) return {true, m <= 16 ? 16 : 32, 128};
   const double q256 = share(256, 256);
-  const bool exact = exact8(m, ld);
+  exact = exact || exact8(m, ld);
   const double t96 = exact ? e96 : 0.1 + 0.3 * q96;
   const double t128 = exact ? e128 : 0.44 * q128 + 0.28 * odd;
   const double t256 = exact ? 3.3 * q256 : 1.55 * q256;
-  if (t96 < t128 && t96 < t256) return {false, 64, 128};
-  return t128 < t256 ? Matmul8Plan{false, 128, 128} : Matmul8Plan{false, 256, 256};
+  if (t96 < t128 && t96 < t256) return {false, 64, 128, exact};
+  return t128 < t256 ? Matmul8Plan{false, 128, 128, exact} : Matmul8Plan{false, 256, 256, exact};
 }
 
 hipError_t launch_linear8(int out, const Linear8Args& a, const Matmul8Plan& p, hipStream_t s) {

@@ -45,6 +45,8 @@ extern "C" {
 int muon_linear8(const muon_tensor8* a, const muon_tensor8* b, const float* bias, int activation,
                  const void* residual, int residual_dtype, long long ldr, void* z, long long ldz,
                  void* y, int y_dtype, long long ldy, const muon_tensor8* y8, hipStream_t stream) {
+  const bool exact = activation >= 0 && (activation & MUON_EXACT);
+  if (exact) activation -= MUON_EXACT;
   if (!tensor8_ok(a) || !tensor8_ok(b) || a->cols != b->cols || !is_activation(activation))
     return MUON_ERR_INVALID_ARG;
   if (!aligned(bias, 4)) return MUON_ERR_INVALID_ARG;
@@ -81,7 +83,7 @@ int muon_linear8(const muon_tensor8* a, const muon_tensor8* b, const float* bias
     g.ld_y8 = ld8(n); g.sld_y8 = scale_ld8(n);
   }
   const int out = y8 ? kOut8 : y_dtype;
-  const Matmul8Plan plan = linear8_plan(out, m, n, g.ld);
+  const Matmul8Plan plan = linear8_plan(out, m, n, g.ld, exact);
   const double dm = m, dn = n, k = a->cols;
   const double bytes = dm * k + dn * k + dm * dn * ((y8 ? 1.0 : (double)ez) + (z ? (double)ez : 0.0) +
                                                     (residual ? (double)size_of(residual_dtype) : 0.0));

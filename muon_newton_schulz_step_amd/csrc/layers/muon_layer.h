@@ -61,6 +61,7 @@ struct Matmul8Args {
 struct Matmul8Plan {
   bool few;  // the kernel for few rows
   int bm, bn;
+  bool exact = false;  // linear8's tiles: products of bf16 values
 };
 Matmul8Plan matmul8_plan(int y_bf16, int m, int n, int ld);
 hipError_t launch_matmul8(int y_bf16, const Matmul8Args& a, const Matmul8Plan& p, hipStream_t s);

@@ -40,6 +40,17 @@ __device__ __forceinline__ float gelu(float z) {
 // (a NaN is below nothing and stays one)
 __device__ __forceinline__ float relu(float z) { return z < 0.f ? 0.f : z; }
 
+// z in front of a factor that is zero far from it, where an infinity (or, in the slopes,
+// a square that overflows) must not meet it.  sigmoid(u) is 0 or 1 in fp32 from |u| =
+// 104 on, so a slope is 0 or 1 beyond +-128 whichever z it is taken at.  A NaN stays
+// one by the other factor.
+__device__ __forceinline__ float above_minus_inf(float z) {
+  return __builtin_fmaxf(z, -0x1.fffffep127f);
+}
+__device__ __forceinline__ float near_zero(float z) {
+  return __builtin_amdgcn_fmed3f(z, -128.f, 128.f);
+}
+
 // u of gelu_tanh: z (1 + tanh(u / 2)) / 2 = z sigmoid(u), u = 2 sqrt(2 / pi) (z + 0.044715 z^3)
 __device__ __forceinline__ float tanh_arg(float z) {
   return z * fmaf(0.071354816f, z * z, 1.5957691f);
@@ -58,13 +69,13 @@ __device__ __forceinline__ void activate(float (&v)[S][N], int act) {
     case MUON_ACT_RELU: each([](float z) { return relu(z); }); break;
     case MUON_ACT_RELU2: each([](float z) { return relu(z) * relu(z); }); break;
     case MUON_ACT_GELU: each([](float z) { return gelu(z); }); break;
-    case MUON_ACT_GELU_TANH: each([](float z) { return z * sigmoid(tanh_arg(z)); }); break;
-    case MUON_ACT_SILU: each([](float z) { return z * sigmoid(z); }); break;
+    case MUON_ACT_GELU_TANH: each([](float z) { return above_minus_inf(z) * sigmoid(tanh_arg(z)); }); break;
+    case MUON_ACT_SILU: each([](float z) { return above_minus_inf(z) * sigmoid(z); }); break;
     default: break;
   }
 }
 
-// d *= act'(z).  At zero relu's slope is 0.
+// d *= act'(z).  At zero relu's slope is 0; at an infinity a slope is its limit there.
 __device__ __forceinline__ void activate_grad(float (&d)[8], const float (&z)[8], int act) {
   if (act == MUON_ACT_RELU) {
     // (a NaN in z is in the result, as it is in the forward pass's)
@@ -79,20 +90,20 @@ __device__ __forceinline__ void activate_grad(float (&d)[8], const float (&z)[8]
       float e;
       const float tail = normal_tail(z[i], e);
       const float c = z[i] > 0.f ? 1.f - tail : tail;
-      d[i] *= fmaf(0.39894228f * z[i], e, c);
+      d[i] *= fmaf(0.39894228f * near_zero(z[i]), e, c);
     }
   } else if (act == MUON_ACT_GELU_TANH) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float s = sigmoid(tanh_arg(z[i]));
-      const float du = fmaf(0.21406445f, z[i] * z[i], 1.5957691f);
-      d[i] *= fmaf(z[i] * (s - s * s), du, s);
+      const float s = sigmoid(tanh_arg(z[i])), b = near_zero(z[i]);
+      const float du = fmaf(0.21406445f, b * b, 1.5957691f);
+      d[i] *= fmaf(b * (s - s * s), du, s);
     }
   } else if (act == MUON_ACT_SILU) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float s = sigmoid(z[i]);
-      d[i] *= fmaf(z[i], s - s * s, s);
+      d[i] *= fmaf(near_zero(z[i]), s - s * s, s);
     }
   }
 }

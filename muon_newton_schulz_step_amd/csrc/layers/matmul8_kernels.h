@@ -121,7 +121,7 @@ __device__ __forceinline__ void epilogue_runs(const Linear8Args& g, const Places
         store_run<FULL, STRM>(
             reinterpret_cast<Z*>(at.z + bytes_away(rows[s], cols, g.ldz, sizeof(Z))), left, v[s]);
   }
-  activate(v, g.act);
+  activate<std::is_same_v<Y, float>>(v, g.act);
   if (R != RES_NONE && g.res) {
 #pragma unroll
     for (int s = 0; s < COUNT; ++s) res[s].add(v[s]);
@@ -159,7 +159,7 @@ __device__ __forceinline__ void epilogue4(const Linear8Args& g, int m, int n, f3
     if (g.z && n + e < g.n)
       static_cast<KeptOf<Y>*>(g.z)[(long long)m * g.ldz + n + e] = from_f32<KeptOf<Y>>(v[0][e]);
   }
-  activate(v, g.act);
+  activate<std::is_same_v<Y, float>>(v, g.act);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     if (g.res && n + e < g.n) {

@@ -46,6 +46,16 @@ __device__ __forceinline__ float columns_of(int w, int cols) {
   return (float)c;
 }
 
+// Zeros past the last column, of which `left` are in front: a finite mean times a finite
+// 1 / sqrt(variance + eps) may be an infinity there, which a weight of zero turns into
+// NaN.  Every row is longer than all of a lane's chunks but the last (with_shape).
+__device__ __forceinline__ void zero_past(float (&v)[8], int left) {
+  if (left < 8) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < left ? v[i] : 0.f;
+  }
+}
+
 // A row's mean and 1 / sqrt(variance + eps); x becomes the deviations.  Each wave
 // takes the mean of its own columns and the squared deviations from that, corrected
 // by the sum of the deviations (which are the mean's rounding), and the team joins
@@ -53,10 +63,11 @@ __device__ __forceinline__ float columns_of(int w, int cols) {
 //   mean = m_0 + sum c_w (m_w - m_0) / n,  sum = sum M_w + c_w (m_w - mean)^2,
 // so that a row of equal values has that value as its mean, exactly.  Lane l of each
 // row of 16 takes wave l's part (`share`: its columns).  `buf` alternates between calls.
+// past: what lies past the last column is used, and becomes zeros.
 template <int TEAM, int NCH>
 __device__ __forceinline__ void row_norm(float (&x)[NCH][8], const int (&col)[NCH], int cols, bool rms,
                                          float eps, float (*buf)[16], int tw, int lane, float own,
-                                         float share, float& mu, float& rstd) {
+                                         float share, bool past, float& mu, float& rstd) {
   const float n = (float)cols;
   float t[2] = {0.f, 0.f};
   mu = 0.f;
@@ -118,9 +129,11 @@ __device__ __forceinline__ void row_norm(float (&x)[NCH][8], const int (&col)[NC
     sum = sum16(l < TEAM ? fmaf(share * e, e, ql) : 0.f);
   }
 #pragma unroll
-  for (int k = 0; k < NCH; ++k)
+  for (int k = 0; k < NCH; ++k) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[k][i] -= mu;
+    if (past && k == NCH - 1) zero_past(x[k], cols - col[k]);
+  }
   rstd = 1.f / sqrtf(sum / n + eps);
 }
 
@@ -202,7 +215,8 @@ __global__ __launch_bounds__(64 * forward_waves(TEAM)) void residual_norm_kernel
     if (row + step < a.rows) fetch(row + step);
     float pmu = 0.f, prstd = 1.f;
     if (post)
-      row_norm<TEAM>(v, col, a.cols, rms, a.p.eps, buf[0], tw, lane, own, share, pmu, prstd);
+      row_norm<TEAM>(v, col, a.cols, rms, a.p.eps, buf[0], tw, lane, own, share, true, pmu,
+                     prstd);
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       constexpr int ONE = LEAN ? 0 : 1;
@@ -213,8 +227,8 @@ __global__ __launch_bounds__(64 * forward_waves(TEAM)) void residual_norm_kernel
       if (a.r) store8_edge(static_cast<X*>(a.r) + row * a.ldr + col[k], a.cols - col[k], v[k]);
     }
     float mu, rstd;
-    row_norm<TEAM>(v, col, a.cols, rms, a.p.eps, buf[post ? 1 : turn], tw, lane, own, share, mu,
-                   rstd);
+    row_norm<TEAM>(v, col, a.cols, rms, a.p.eps, buf[post ? 1 : turn], tw, lane, own, share, false,
+                   mu, rstd);
     turn ^= 1;
     if (tw == 0 && lane == 0) {
       a.stats[row] = mu;
@@ -273,6 +287,9 @@ residual_back_kernel(ResidualBackArgs a) {
   // their next one, as fp32 rows of several chunks, when its turn comes
   constexpr bool LEAN = TEAM * NCH > 16;
   constexpr bool EARLY = NCH == 1 || (XT == MUON_BF16 && !LEAN);
+  // Chunks that zero_past is asked about: the last one.  Rows too long for the registers
+  // spill less with its branch in both (2048 x 16384, branch parameters: 337 us and 459).
+  constexpr auto EDGE = [](int k) { return LEAN || k == NCH - 1; };
   __shared__ float buf[2][TEAMS][2][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int tw = wave % TEAM, team = wave / TEAM;
@@ -381,16 +398,18 @@ residual_back_kernel(ResidualBackArgs a) {
         add(std::integral_constant<int, 1>{}, kk, d[k]);
         constexpr int kw = LEAN ? 0 : k;
         if constexpr (LEAN) load8_edge(a.p.weight + col[k], a.cols - col[k], w[0]);
-        // past the last column dh, x and the weights are zeros, so whatever rh and
-        // bh come to there, no sum over the row gets anything from it
+        // past the last column dh, x and the weights are zeros, and rh, d and bh are
+        // made so: no sum over the row gets anything from it
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[k][i] = (x[k][i] - mu) * r;
+        if constexpr (EDGE(k)) zero_past(x[k], a.cols - col[k]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float rh = (x[k][i] - mu) * r;
+          const float rh = x[k][i];
           p[i] = d[k][i] * rh;
           const float g = d[k][i] * w[kw][i];
           c[0] += g;
           c[1] = fmaf(g, rh, c[1]);
-          x[k][i] = rh;
           d[k][i] = g;
         }
         add(std::integral_constant<int, 0>{}, kk, p);
@@ -415,19 +434,25 @@ residual_back_kernel(ResidualBackArgs a) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) dr[i] = 0.f;
         }
-        if constexpr (BRANCH) rb[k].get(bh[k]);
+        if constexpr (BRANCH) {
+          rb[k].get(bh[k]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) bh[k][i] = (bh[k][i] - pmu) * pr;
+          if constexpr (EDGE(k)) zero_past(bh[k], a.cols - col[k]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d[k][i] = fmaf(r, d[k][i] - c0 - x[k][i] * c1, dr[i]);
+        if constexpr (EDGE(k)) zero_past(d[k], a.cols - col[k]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float v = fmaf(r, d[k][i] - c0 - x[k][i] * c1, dr[i]);
-          d[k][i] = v;
+          const float v = d[k][i];
           if (a.g.scale && i % 2) dscale += (double)fmaf(v, xs[i], d[k][i - 1] * xs[i - 1]);
           if constexpr (BRANCH) {
-            const float h = (bh[k][i] - pmu) * pr;
+            const float h = bh[k][i];
             p[i] = v * h;
             const float g = v * wp[kw][i];
             e[0] += g;
             e[1] = fmaf(g, h, e[1]);
-            bh[k][i] = h;
           }
         }
         if constexpr (BRANCH) {

@@ -3,6 +3,7 @@
 // launches.
 #include <hip/hip_runtime_api.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "muon.h"
@@ -194,7 +195,9 @@ size_t muon_residual_norm_backward_workspace_bytes(int rows, int cols, int branc
   if (rows < 1 || rows > MUON_MAX_ROWS || cols < 1 || cols > MUON_MAX_NORM_COLS ||
       (branch_params != 0 && branch_params != 1))
     return 0;
-  const int groups = residual_back_groups(rows, cols, branch_params);
+  // (of either type, which the query does not know)
+  const int groups = std::max(residual_back_groups(rows, cols, branch_params, false),
+                              residual_back_groups(rows, cols, branch_params, true));
   return scale_parts_bytes(groups) +
          (size_t)groups * (branch_params ? 4 : 2) * (size_t)cols * sizeof(float);
 }
@@ -251,7 +254,7 @@ int muon_residual_norm_backward(const void* dr, long long lddr, const void* dh, 
   a.b = branch; a.ldb = ldb; a.x = x; a.ldx = ldx; a.rows = rows; a.cols = cols;
   a.p = *params; a.stats = stats; a.dx = dx; a.lddx = lddx; a.db = dbranch; a.lddb = lddb;
   a.g = *grads; a.accumulate = accumulate;
-  a.groups = rows > 0 ? residual_back_groups(rows, cols, of_branch) : 0;
+  a.groups = rows > 0 ? residual_back_groups(rows, cols, of_branch, branch_dtype == MUON_FP32) : 0;
   if (need) {
     a.part_scale = static_cast<double*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + scale_parts_bytes(a.groups));

@@ -92,7 +92,7 @@ struct ResidualBackArgs {
 };
 // Whether the branch's parameters have gradients: four sums per column, not two.
 inline bool residual_branch(const muon_residual_params& p) { return p.post_weight || p.gate; }
-int residual_back_groups(int rows, int cols, bool branch);
+int residual_back_groups(int rows, int cols, bool branch, bool b_fp32);
 hipError_t launch_residual_norm_backward(int x_bf16, int b_bf16, const ResidualBackArgs& a,
                                          hipStream_t s);
 

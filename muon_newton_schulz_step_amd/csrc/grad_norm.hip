@@ -8,10 +8,13 @@
 // Tensors are cut into tiles; a workgroup takes a run of neighbouring tiles,
 // finds its first one's tensor by bisection and goes on from there, so that many
 // small tensors and a few large ones share a launch evenly.  Each workgroup
-// leaves one sum; the finishing launch, or each workgroup of the clipping one,
-// adds those in their order.  The clipping pass goes over its run backwards:
-// what the norm read last is what the last-level cache still holds, and its
-// results are stored past that.
+// leaves one sum, and the finishing launch adds those in their order.  Up to as many as
+// one launch can have, 2048, each workgroup of a clipping launch adds them itself, which
+// saves that launch (129 tensors of 100003 numbers, not clipped: 22.0 us, 23.4 with it);
+// more would be a work that grows with the square of the tensors, and the clipping ones
+// take the finishing one's sum (4000 of 2^18: 805 us, 2670 without; 300 of them 62, 69).
+// The clipping pass goes over its run backwards: what the norm read last is what the
+// last-level cache still holds, and its results are stored past that.
 //   805e6 numbers, fp32: norm 540 us (6.0 TB/s; a copy runs at 5.2), clipped into
 //   bf16 1482 us (5.4 TB/s over two readings and the writing); bf16: norm 273 us
 //   (5.9), clipped 939 us (5.1).  With half the workgroups and cached stores 600,
@@ -108,21 +111,26 @@ __global__ __launch_bounds__(kClipThreads) void norm_parts_kernel(ClipLaunch) {
 // All launches' sums, each thread every 512th, so the order is always the same.
 __device__ __forceinline__ double sum_parts(const double* part, int parts, double* buf) {
   double s = 0.0;
+#pragma unroll 8
   for (int j = threadIdx.x; j < parts; j += kClipThreads) s += part[j];
-  return sqrt(block_sum<kClipThreads / 64>(s, buf));
+  return block_sum<kClipThreads / 64>(s, buf);
 }
 
-__global__ __launch_bounds__(kClipThreads) void norm_finish_kernel(const double* part, int parts,
-                                                                   float* norm) {
+// keep: the sum takes the first part's place, which block_sum's barrier leaves free.
+__global__ __launch_bounds__(kClipThreads) void norm_finish_kernel(double* part, int parts,
+                                                                   float* norm, bool keep) {
   __shared__ double buf[kClipThreads / 64];
-  const double n = sum_parts(part, parts, buf);
-  if (threadIdx.x == 0) *norm = (float)n;
+  const double s = sum_parts(part, parts, buf);
+  if (threadIdx.x == 0) {
+    *norm = (float)sqrt(s);
+    if (keep) *part = s;
+  }
 }
 
 __global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipLaunch) {
   const auto& a = kernarg<ClipLaunch>();
   __shared__ double buf[kClipThreads / 64];
-  const double norm = sum_parts(a.part, a.parts, buf);
+  const double norm = sqrt(sum_parts(a.part, a.parts, buf));
   if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
   const double q = (double)a.max_norm / (norm + (double)a.eps);
   // A NaN stays one.  A c below fp32's normal numbers would have lost digits:
@@ -168,8 +176,8 @@ hipError_t launch_norm_parts(const ClipLaunch& a, hipStream_t s) {
   hipLaunchKernelGGL(norm_parts_kernel, dim3(a.groups), dim3(kClipThreads), 0, s, a);
   return hipGetLastError();
 }
-hipError_t launch_norm_finish(const double* part, int parts, float* norm, hipStream_t s) {
-  hipLaunchKernelGGL(norm_finish_kernel, dim3(1), dim3(kClipThreads), 0, s, part, parts, norm);
+hipError_t launch_norm_finish(double* part, int parts, float* norm, bool keep, hipStream_t s) {
+  hipLaunchKernelGGL(norm_finish_kernel, dim3(1), dim3(kClipThreads), 0, s, part, parts, norm, keep);
   return hipGetLastError();
 }
 hipError_t launch_clip(const ClipLaunch& a, hipStream_t s) {

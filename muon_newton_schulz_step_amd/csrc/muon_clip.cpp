@@ -133,12 +133,15 @@ int clip_impl(int n, const long long* sizes, const void* const* grads, const int
       if (err == hipSuccess) err = launch_norm_parts(a, stream);
     });
     if (err != hipSuccess) return err;
-    if (!clip || parts == 0) return launch_norm_finish(part, parts, norm, stream);
+    // no more sums than one launch can have: clipping's workgroups add them
+    const bool few = clip && parts > 0 && parts <= kClipGroups;
+    if (!few) err = launch_norm_finish(part, parts, norm, clip && parts > 0, stream);
+    if (err != hipSuccess || !clip) return err;
     a.part = part;
-    a.parts = parts;
+    a.parts = few ? parts : 1;
     a.max_norm = max_norm;
     a.eps = eps;
-    a.norm = norm;
+    a.norm = few ? norm : nullptr;
     each_launch(n, sizes, [&](int from, int to, long long tiles) {
       fill(from, to, tiles);
       if (err == hipSuccess) err = launch_clip(a, stream);

@@ -27,14 +27,15 @@ struct ClipTable {
 struct ClipLaunch {
   ClipTable t;
   int tensors, groups;
-  double* part;      // norm: this launch's sums; clip: those of all launches
-  int parts;         // clip: of all launches
+  double* part;      // norm: this launch's sums; clip: all launches', or their sum
+  int parts;         // clip: how many
   float max_norm, eps;
   float* norm;       // written by the finishing launch, or by clip's first one
 };
 
 hipError_t launch_norm_parts(const ClipLaunch& a, hipStream_t s);
-hipError_t launch_norm_finish(const double* part, int parts, float* norm, hipStream_t s);
+// keep: part[0] becomes the sum of all parts
+hipError_t launch_norm_finish(double* part, int parts, float* norm, bool keep, hipStream_t s);
 hipError_t launch_clip(const ClipLaunch& a, hipStream_t s);
 
 }  // namespace muon

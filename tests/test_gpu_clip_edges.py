@@ -1,0 +1,58 @@
+"""Clipping of many tensors at once."""
+import pytest
+import torch
+
+import muon_newton_schulz_step_amd as mn
+from gpu_helpers import announce
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+BF16, FP32 = torch.bfloat16, torch.float32
+
+
+def kernels_ms(f):
+    """The least time of a call's kernels, from the timing log."""
+    times = []
+    for _ in range(6):
+        mn.timing_read()
+        mn.timing_enable(True)
+        try:
+            f()
+            torch.cuda.synchronize()
+            (r,) = mn.timing_read()
+        finally:
+            mn.timing_enable(False)
+        times.append(r["ms"])
+    return min(times)
+
+
+def many(count, size):
+    flat = torch.zeros(count * size, dtype=BF16, device=DEV)
+    flat[::size] = 1.0
+    return flat, list(flat.split(size))
+
+
+def test_many_tensors():
+    """Launches of 128 tensors each: the norm, clipped results and repeats."""
+    announce("clip: 1500 tensors")
+    flat, grads = many(1500, 20_001)
+    kept = flat.clone()
+    norm = mn.clip_grads(grads, 1.0)
+    assert float(norm) == float(mn.grad_norm(list(kept.split(20_001)))) == float(torch.tensor(1500.0).sqrt())
+    c = torch.tensor(1.0 / (1500.0 ** 0.5 + 1e-6), dtype=torch.float64).to(FP32)
+    assert torch.equal(flat, (kept.float() * c).to(BF16))
+    again = kept.clone()
+    assert torch.equal(mn.clip_grads(list(again.split(20_001)), 1.0), norm) and torch.equal(again, flat)
+    out = torch.zeros_like(kept)
+    assert torch.equal(mn.clip_grads(list(kept.split(20_001)), 1.0, out=list(out.split(20_001))), norm)
+    assert torch.equal(out, flat)
+
+
+def test_work_grows_with_the_tensors():
+    """Gradients that stay as they are cost the clipping pass next to nothing, however many
+    launches there are: at most as much again as their norm."""
+    announce("clip: 4000 tensors of 262144")
+    _, grads = many(4000, 1 << 18)
+    norm, clip = kernels_ms(lambda: mn.grad_norm(grads)), kernels_ms(lambda: mn.clip_grads(grads, 1e6))
+    print("norm", norm, "ms, clip", clip, "ms")
+    assert clip <= 2.5 * norm

@@ -132,7 +132,8 @@ __global__ __launch_bounds__(kClipThreads) void clip_kernel(ClipLaunch) {
   __shared__ double buf[kClipThreads / 64];
   const double norm = sqrt(sum_parts(a.part, a.parts, buf));
   if (a.norm && blockIdx.x == 0 && threadIdx.x == 0) *a.norm = (float)norm;
-  const double q = (double)a.max_norm / (norm + (double)a.eps);
+  // (0 / 0, for gradients of zeros without an eps, is not below 1: they stay)
+  const double over = norm + (double)a.eps, q = over == 0.0 ? 1.0 : (double)a.max_norm / over;
   // A NaN stays one.  A c below fp32's normal numbers would have lost digits:
   // it is applied as two factors, the second a power of two.
   const bool tiny = q < 0x1p-126;

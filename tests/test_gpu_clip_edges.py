@@ -1,4 +1,4 @@
-"""Clipping of many tensors at once."""
+"""Clipping to a limit of zero without eps, and of many tensors at once."""
 import pytest
 import torch
 
@@ -8,6 +8,22 @@ from gpu_helpers import announce
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 BF16, FP32 = torch.bfloat16, torch.float32
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_zeros_without_eps(dtype):
+    """0 / 0 is not below 1: the gradients, all zeros, stay as they are."""
+    announce("clip: zeros, a limit of zero, no eps", dtype)
+    g = torch.zeros(40_000, dtype=dtype, device=DEV)
+    g[7] = -0.0
+    kept, out = g.clone(), torch.full_like(g, 5.0)
+    for limit in (0.0, 1.0):
+        assert float(mn.clip_grads([g], limit, eps=0.0, out=[out])) == 0.0
+        assert torch.equal(out, kept)
+        assert float(mn.clip_grads([g], limit, eps=0.0)) == 0.0
+        assert torch.equal(g, kept)
+    g[3] = 2.0                                                # and a limit of zero is still one
+    assert float(mn.clip_grads([g], 0.0, eps=0.0)) == 2.0 and (g == 0).all()
 
 
 def kernels_ms(f):

@@ -8,7 +8,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmuon.so")
 
 MUON_BF16, MUON_FP32 = 0, 1
-MUON_EXACT = 0x100
+MUON_EXACT, MUON_FAST = 0x100, 0x200
 ACTIVATIONS = {None: 0, "relu": 1, "relu2": 2, "gelu": 3, "gelu_tanh": 4, "silu": 5}
 MUON_OK, MUON_ERR_INVALID_ARG, MUON_ERR_UNSUPPORTED, MUON_ERR_WORKSPACE, MUON_ERR_HIP = 0, -1, -2, -3, -4
 MUON_MAX_STEPS = 64

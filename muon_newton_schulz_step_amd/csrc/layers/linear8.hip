@@ -7,19 +7,22 @@ namespace muon {
 namespace {
 constexpr int kOut8 = 2;
 
-// Whether an 8-bit result comes from exact products where its caller leaves that open
-// (one that asks for them gets them at every size).  Rounding to 8 bits turns an
-// error of relative size e into flips of a whole step, 2^-4, for a share e / 2^-4 of the
-// values: sqrt(e 2^-4) in the norm.  The 8-bit instruction's cut leaves e near 1e-4
-// where a few columns of a are 64 times the others, and more where the sum is short
-// and few of them share it: an MLP's result (squared ReLU, those columns 1% of all) was
-// off by 6.2e-3 of its norm for 200 rows of 128, 5.6e-3 for 60 of 520, 3 to 3.7e-3 for
-// thousands of rows and 520 or more columns; with exact products by 1.7e-3, what its
-// rounding to bf16 does.  Exact costs 99 us against 74 (8192 x 8192 x 512), 26 against
-// 20 (8192 x 2048 x 512), 14 against 12 (512 x 5120 x 1280), but 62 against 35 at 512 x
-// 16384 x 4096.  By its caller's choice: the up projection of an MLP with z kept 43 ->
-// 58 us (4096 x 5120 x 1280) and 979 -> 1705 (16384 x 16384 x 4096), its result off by
-// 1.7e-3 instead of 3.0e-3 and 2.4e-3.
+// Rounding to 8 bits turns a product's error of relative size e into flips of a whole
+// step, 2^-4, for a share e / 2^-4 of the values: sqrt(e 2^-4) in the norm.  The 8-bit
+// instruction's cut leaves e near 1e-4 where a few columns of a are 64 times the others,
+// and more where the sum is short and few of them share it.  A hidden layer in 8 bits was
+// off from that of exact products by 1.7e-3 to 2.2e-3 of its norm with every activation
+// and 2.3e-3 to 2.8e-3 with the squared ReLU, which doubles e (4096 x 1280, 600 x 700, 2000
+// x 528, 1024 x 4096, those columns 1% of all), an MLP's result by 2.4e-3 to 3.7e-3
+// and, of 200 rows of 128, 6.2e-3 where with exact products its rounding to bf16 leaves
+// 1.7e-3.  So 8-bit results come from exact products unless their caller chose speed
+// (fast): the up projection of an MLP with z kept takes 58 us instead of 43 (4096 x
+// 5120 x 1280) and 1705 instead of 979 (16384 x 16384 x 4096).
+//
+// A plain product in 8 bits, without bias, activation, residual and z, is muon_matmul8's
+// with its result rounded once more, cut as that is, but where exact products cost
+// little: 99 us against 74 (8192 x 8192 x 512), 26 against 20 (8192 x 2048 x 512), 14
+// against 12 (512 x 5120 x 1280).
 bool exact8(int m, int ld) { return ld <= 512 || (m <= 512 && ld <= 1280); }
 
 template <int BM, int BN, int WGM, int WGN, bool EXACT, typename Y>
@@ -81,14 +84,17 @@ void go(const Linear8Args& a, const Matmul8Plan& p, hipStream_t s) {
 // with one of 64 x 128 beside the others for results in fp32 and 8 bits: of those a CU
 // holds three, which fill the last round of a middle-sized grid better.  Measured at
 // 100 to 16384 rows, 768 to 5120 columns and sums of 700 to 5120 (in us; fp32 with a
-// residual, 8 bits with z kept):
+// residual, 8 bits with z kept, of cut products):
 //   fp32    4099 x 1280 x 5120 65.4 -> 57.7, 1027 x 5120 x 1280 25.2 -> 21.4, 300 x 4096
 //           x 4096 27.2 -> 22.5; but 16384 x 1280 x 5120 184 against 193
 //   8 bits  600 x 1280 x 5120 33.3 -> 26.5, 4099 x 768 x 3080 23.6 -> 20.2; but 2048 x
-//           4096 x 4096 35.4 against 52.6
+//           4096 x 4096 35.4 against 52.6.  Exact, the fastest of the three or within 3% at
+//           14 sizes of 1024 to 16384 rows: 1200 x 5000 x 1300 23.8 (128: 25.7, 256: 40.2),
+//           4096 x 5120 x 1280 58 (62, 78), 16384 x 16384 x 4096 1640 (1977, 1850)
 // In bf16 it gains at few sizes (4099 x 768 x 3080 21.8 -> 18.7) and is not taken, but
 // for exact products, whose costs are those of a result in fp32.
-Matmul8Plan linear8_plan(int out, int m, int n, int ld, bool exact) {
+Matmul8Plan linear8_plan(int out, int m, int n, int ld, Products products) {
+  bool exact = products == kExact;
   auto share = [&](int bm, int bn) {  // tiles of the fullest CU
     return (double)(((long long)((m + bm - 1) / bm) * ((n + bn - 1) / bn) + 255) / 256);
   };
@@ -107,7 +113,7 @@ Matmul8Plan linear8_plan(int out, int m, int n, int ld, bool exact) {
   // An 8-bit result needs whole blocks of 128 columns in a workgroup.
   if (m <= 32) return {true, m <= 16 ? 16 : 32, 128};
   const double q256 = share(256, 256);
-  exact = exact || exact8(m, ld);
+  if (products == kMatmul8) exact = exact8(m, ld);
   const double t96 = exact ? e96 : 0.1 + 0.3 * q96;
   const double t128 = exact ? e128 : 0.44 * q128 + 0.28 * odd;
   const double t256 = exact ? 3.3 * q256 : 1.55 * q256;

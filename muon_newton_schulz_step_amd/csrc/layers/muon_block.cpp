@@ -46,8 +46,10 @@ extern "C" {
 int muon_linear8(const muon_tensor8* a, const muon_tensor8* b, const float* bias, int activation,
                  const void* residual, int residual_dtype, long long ldr, void* z, long long ldz,
                  void* y, int y_dtype, long long ldy, const muon_tensor8* y8, hipStream_t stream) {
-  const bool exact = activation >= 0 && (activation & MUON_EXACT);
-  if (exact) activation -= MUON_EXACT;
+  const int choice = activation > 0 ? activation & (MUON_EXACT | MUON_FAST) : 0;
+  activation -= choice;
+  if (choice == (MUON_EXACT | MUON_FAST) || (choice == MUON_FAST && !y8 && y_dtype == MUON_FP32))
+    return MUON_ERR_INVALID_ARG;
   if (!tensor8_ok(a) || !tensor8_ok(b) || a->cols != b->cols || !is_activation(activation))
     return MUON_ERR_INVALID_ARG;
   if (!aligned(bias, 4)) return MUON_ERR_INVALID_ARG;
@@ -84,7 +86,12 @@ int muon_linear8(const muon_tensor8* a, const muon_tensor8* b, const float* bias
     g.ld_y8 = ld8(n); g.sld_y8 = scale_ld8(n);
   }
   const int out = y8 ? kOut8 : y_dtype;
-  const Matmul8Plan plan = linear8_plan(out, m, n, g.ld, exact);
+  // what is rounded to 8 bits behind an epilogue is exact by itself
+  const bool fused = bias || activation != MUON_ACT_NONE || residual || z;
+  const Products products = choice == MUON_FAST                    ? kFast
+                            : choice == MUON_EXACT || (y8 && fused) ? kExact
+                                                                    : kMatmul8;
+  const Matmul8Plan plan = linear8_plan(out, m, n, g.ld, products);
   const double dm = m, dn = n, k = a->cols;
   const double bytes = dm * k + dn * k + dm * dn * ((y8 ? 1.0 : (double)ez) + (z ? (double)ez : 0.0) +
                                                     (residual ? (double)size_of(residual_dtype) : 0.0));

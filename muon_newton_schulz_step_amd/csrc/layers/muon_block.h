@@ -19,8 +19,11 @@ struct Linear8Args : Matmul8Args {
   unsigned char* s8;
   long long ld_y8, sld_y8;
 };
-// out: MUON_BF16, MUON_FP32, or 2 for the 8-bit result; exact: asked for by the caller
-Matmul8Plan linear8_plan(int out, int m, int n, int ld, bool exact);
+// Products of many rows: those of muon_matmul8 for a result of this type, exact ones, or
+// the 8-bit instruction's.
+enum Products { kMatmul8, kExact, kFast };
+// out: MUON_BF16, MUON_FP32, or 2 for the 8-bit result
+Matmul8Plan linear8_plan(int out, int m, int n, int ld, Products products);
 hipError_t launch_linear8(int out, const Linear8Args& a, const Matmul8Plan& p, hipStream_t s);
 
 // dz = dy act'(z) in bf16 and in 8 bits, and its sum over the rows

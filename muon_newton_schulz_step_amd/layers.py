@@ -23,7 +23,8 @@ from __future__ import annotations
 import threading
 
 from . import _lib
-from . import MUON_BF16, MUON_EXACT, MUON_FP32, MUON_OK, MuonError, Workspace, _workspace_tensor, lib
+from . import (MUON_BF16, MUON_EXACT, MUON_FAST, MUON_FP32, MUON_OK, MuonError, Workspace,
+               _workspace_tensor, lib)
 
 _MAX_ROWS = _lib.MUON_MAX_ROWS
 
@@ -321,7 +322,7 @@ def _activation(name) -> int:
 
 
 def linear8(a, b, bias=None, *, activation=None, residual=None, keep: bool = False,
-            out_dtype=None, out=None, exact: bool = False):
+            out_dtype=None, out=None, exact=None):
     """act(a b^T + bias) + residual of two Tensor8, (m, k) and (n, k) -> (m, n) in
     bf16 (default), fp32, or torch.float8_e4m3fn: a Tensor8 with blocks of
     1 x 128, the next product's operand.  ``bias`` is fp32, ``residual`` bf16 or fp32;
@@ -329,16 +330,17 @@ def linear8(a, b, bias=None, *, activation=None, residual=None, keep: bool = Fal
     "silu".  ``keep`` returns (y, z) with z = a b^T + bias for linear8_backward, in
     y's dtype (bf16 beside a Tensor8).  ``out`` may be given: a matrix in bf16 or fp32,
     which may have a row stride, or a Tensor8.
-    Everything is fp32 up to the one rounding of each result; the sums are those
-    of matmul8, in bf16 and of many rows from the 8-bit matrix instruction, which cuts
-    small products beside large ones.  In 8 bits that turns values close to halfway to
-    their other neighbour: such a result's products are exact where sums are short or
-    rows few (include/muon.h has the sizes), and ``exact`` makes them so at every size
-    and for every result, whatever the batch, at up to twice the time."""
+    Everything is fp32 up to the one rounding of each result.  Products are exact, but
+    for bf16 results of many rows, which are those of matmul8 and cut far below their
+    rounding, and for plain ones in 8 bits (without bias, activation, residual and
+    ``keep``).  ``exact`` True makes these exact as well; False takes matmul8's for every
+    8-bit result, up to 1.7 times as fast, but more of its values close to halfway go to
+    their other neighbour (include/muon.h has the figures)."""
     torch = _T or _torch()
     if a.cols != b.cols:
         raise ValueError(f"a and b must have the same number of columns: {a.cols}, {b.cols}")
     act = _activation(activation)
+    flags = 0 if exact is None else MUON_EXACT if exact else MUON_FAST
     if keep and not act:
         raise ValueError("keep is for an activation: without one the backward pass needs no z")
     m, n = a.rows, b.rows
@@ -369,11 +371,14 @@ def linear8(a, b, bias=None, *, activation=None, residual=None, keep: bool = Fal
             raise ValueError("out must be (a.rows, b.rows) and of out_dtype")
         yp, _, _, ldy = _matrix(out, "out") if n else (0, m, n, 1)
         code, y8 = _dtype_code(out.dtype), None
+    if flags == MUON_FAST and not out8 and code == MUON_FP32:
+        raise ValueError("a result in fp32 comes from exact products")
     z = zp = None
     if keep:
         z = torch.empty(m, n, dtype=torch.bfloat16 if out8 else out.dtype, device=device)
         zp = z.data_ptr()
-    _call(index, "muon_linear8", a._c, b._c, bp, act + MUON_EXACT if exact else act, rp, rcode, ldr, zp, n, yp, code, ldy, y8)
+    _call(index, "muon_linear8", a._c, b._c, bp, act + flags, rp, rcode, ldr, zp, n, yp, code, ldy,
+          y8)
     return (out, z) if keep else out
 
 

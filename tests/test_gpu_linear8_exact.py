@@ -48,14 +48,32 @@ def check(got, kept, z, out):
         assert np.array_equal(to64(got), rounded(y, out))
 
 
-# on the limits up to which an 8-bit result's products are exact by themselves
 @pytest.mark.parametrize("m,n,k", [(1, 130, 5000), (16, 260, 1300), (17, 300, 2000), (32, 140, 5120), (33, 140, 1280),
                                    (512, 300, 1280), (300, 1300, 900), (513, 200, 512), (2100, 2050, 500),
-                                   (2560, 4097, 512)])
-def test_short_sums_and_few_rows(m, n, k):
+                                   (2560, 4097, 512), (513, 300, 1290), (600, 1300, 700), (2100, 2050, 600),
+                                   (8192, 4096, 520)])
+def test_8_bits_are_exact_by_themselves(m, n, k):
     announce("linear8 to 8 bits, exact by itself", m, n, k)
     a, b, z = operands(m, n, k)
     check(*mn.linear8(a, b, activation="relu2", keep=True, out_dtype=E4M3), z, E4M3)
+    zero = torch.zeros(n, device=DEV)
+    for kw in (dict(bias=zero), dict(residual=zero.expand(m, -1).contiguous()), dict(activation="relu")):
+        got = mn.linear8(a, b, out_dtype=E4M3, **kw)
+        q, e = lo.quantize8(np.maximum(z, 0) if "activation" in kw else z, 1)
+        assert np.array_equal(got.scale.cpu().numpy()[:, :e.shape[1]].astype(np.int64) - 127, e)
+        assert np.array_equal(to64(got.data.float())[:, :n], q)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 130, 5000), (32, 140, 5120), (512, 300, 1280), (513, 200, 512),
+                                   (2560, 4097, 512)])
+def test_plain_short_sums_and_few_rows(m, n, k):
+    """On the limits up to which a plain product in 8 bits is exact by itself."""
+    announce("linear8 to 8 bits, plain", m, n, k)
+    a, b, z = operands(m, n, k)
+    got = mn.linear8(a, b, out_dtype=E4M3)
+    q, e = lo.quantize8(z, 1)
+    assert np.array_equal(got.scale.cpu().numpy()[:, :e.shape[1]].astype(np.int64) - 127, e)
+    assert np.array_equal(to64(got.data.float())[:, :n], q)
 
 
 # every kernel and tile that the rules pick for exact products
@@ -89,18 +107,45 @@ def test_rows_do_not_depend_on_the_batch():
     announce("linear8 exact: batches")
     a, b, _ = operands(1100, 300, 1300, seed=5)
     x, bias = a.dequantize(FP32), torch.full((300,), 0.37, device=DEV)
-    ref = mn.linear8(a, b, bias, activation="gelu", out_dtype=E4M3, exact=True)
+    ref = mn.linear8(a, b, bias, activation="gelu", out_dtype=E4M3)
     for m in (1, 20, 512, 513):
-        part = mn.linear8(mn.quantize8(x[:m].contiguous()), b, bias, activation="gelu", out_dtype=E4M3, exact=True)
+        part = mn.linear8(mn.quantize8(x[:m].contiguous()), b, bias, activation="gelu", out_dtype=E4M3)
         assert torch.equal(part.data.view(torch.uint8), ref.data.view(torch.uint8)[:m])
         assert torch.equal(part.scale, ref.scale[:m])
 
 
-def test_otherwise_those_of_a_bf16_result():
-    announce("linear8 to 8 bits: products of a bf16 result")
-    for m, n, k in ((513, 300, 1290), (600, 1300, 700), (2560, 4097, 600)):
-        g = torch.Generator(DEV).manual_seed(m)
-        a = mn.quantize8(torch.randn(m, k, generator=g, device=DEV))
-        b = mn.quantize8(torch.randn(n, k, generator=g, device=DEV), 128)
-        kept = [mn.linear8(a, b, activation="silu", keep=True, out_dtype=out)[1] for out in (BF16, E4M3)]
-        assert torch.equal(*kept)
+# every tile that the rules pick for the 8-bit instruction's products in 8 bits
+FAST = [(600, 1300, 1290, (64, 128)), (2100, 2050, 140, (128, 128)), (2560, 4097, 600, (256, 256)),
+        (33, 260, 130, (64, 128))]
+
+
+@pytest.mark.parametrize("m,n,k,tile", FAST)
+def test_fast_by_choice(m, n, k, tile):
+    """Those of a bf16 result: z of real numbers is the same, and small whole numbers, of
+    which the instruction cuts nothing, give the exact 8 bits."""
+    announce("linear8 to 8 bits, fast", m, n, k)
+    g = torch.Generator(DEV).manual_seed(m)
+    a = mn.quantize8(torch.randn(m, k, generator=g, device=DEV))
+    b = mn.quantize8(torch.randn(n, k, generator=g, device=DEV), 128)
+    kept = [mn.linear8(a, b, activation="silu", keep=True, out_dtype=out, exact=False)[1] for out in (BF16, E4M3)]
+    assert torch.equal(*kept)
+    assert torch.equal(kept[0], mn.linear8(a, b, activation="silu", keep=True)[1])
+    av, bv = whole(m, k, seed=1), whole(n, k, seed=2)
+    a, b, bias = mn.quantize8(av), mn.quantize8(bv, 128), whole(n, seed=3, top=9)
+    res = whole(m, n, seed=4, top=50).to(BF16)
+    mn.timing_read()
+    mn.timing_enable(True)
+    try:
+        got = mn.linear8(a, b, bias, activation="relu2", residual=res, out_dtype=E4M3, exact=False)
+        torch.cuda.synchronize()
+        (r,) = mn.timing_read()
+    finally:
+        mn.timing_enable(False)
+    pad = lambda v, t: -(-v // t) * t  # noqa: E731
+    assert r["exec_flops"] == 2.0 * pad(m, tile[0]) * pad(n, tile[1]) * pad(k, 128)
+    y = lo.activation(to64(av) @ to64(bv).T + to64(bias), "relu2") + to64(res)
+    q, e = lo.quantize8(y, 1)
+    assert np.array_equal(got.scale.cpu().numpy()[:, :e.shape[1]].astype(np.int64) - 127, e)
+    assert np.array_equal(to64(got.data.float())[:, :n], q)
+    with pytest.raises(ValueError):
+        mn.linear8(a, b, out_dtype=FP32, exact=False)

@@ -1,17 +1,31 @@
-"""linear8's choice of exact products without a GPU: its flag in the C ABI, and that the
-operands of tests/test_gpu_linear8_exact.py tell exact products from cut ones."""
+"""linear8's choice of products without a GPU: its flags in the C ABI, and that the operands
+of tests/test_gpu_linear8_exact.py tell exact products from cut ones."""
 import numpy as np
+import pytest
 
 import muon_newton_schulz_step_amd as mn
 from test_linear8_cpu import INVALID, OK, P, forward, t8
 
 
-def test_flag():
-    exact = mn.MUON_EXACT
+def test_flags():
+    exact, fast = mn.MUON_EXACT, mn.MUON_FAST
     for act in range(6):
-        assert forward(act=act | exact, a=t8(1, 0)) == OK
-    assert forward(act=6 | exact) == forward(act=exact << 1) == forward(act=-exact) == INVALID
-    assert forward(act=exact, y=P) == INVALID                     # its other checks stay
+        assert forward(act=act | exact, a=t8(1, 0)) == forward(act=act | fast, a=t8(1, 0)) == OK
+        assert forward(act=act | exact, dtype=mn.MUON_FP32, a=t8(1, 0)) == OK
+        assert forward(act=act | fast, dtype=mn.MUON_FP32, a=t8(1, 0)) == INVALID
+        assert forward(act=act | fast | exact, a=t8(1, 0)) == INVALID
+    y8 = t8(3, 0, 16)
+    assert forward(act=fast, dtype=mn.MUON_FP32, y=0, y8=y8, a=t8(1, 0)) == OK
+    assert forward(act=6 | exact) == forward(act=6 | fast) == forward(act=fast << 1) == INVALID
+    assert forward(act=-exact) == forward(act=-fast) == forward(act=exact - 1) == INVALID
+    assert forward(act=exact, y=P) == forward(act=fast, y=P) == INVALID  # its other checks stay
+
+
+def test_binding_refusals():
+    a, b = mn.Tensor8.empty(8, 256, device="cpu"), mn.Tensor8.empty(16, 256, 128, device="cpu")
+    for exact in (True, False, None):
+        with pytest.raises(ValueError):            # not on a GPU
+            mn.linear8(a, b, exact=exact)
 
 
 def cut(a, b):

@@ -72,3 +72,21 @@ def test_work_grows_with_the_tensors():
     norm, clip = kernels_ms(lambda: mn.grad_norm(grads)), kernels_ms(lambda: mn.clip_grads(grads, 1e6))
     print("norm", norm, "ms, clip", clip, "ms")
     assert clip <= 2.5 * norm
+
+
+def test_many_tensors_captured():
+    announce("clip: 1500 tensors, captured")
+    flat, grads = many(1500, 20_001)
+    out = torch.zeros_like(flat)
+    outs = list(out.split(20_001))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norm = mn.clip_grads(grads, 1.0, out=outs)
+    for k in (2.0, 0.25, 8.0):
+        flat.mul_(k)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got, clipped = norm.clone(), out.clone()
+        assert torch.equal(mn.clip_grads(grads, 1.0, out=outs), got) and torch.equal(out, clipped)
+        assert float(got) == float(mn.grad_norm(grads))

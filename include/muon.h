@@ -327,7 +327,8 @@ typedef enum {
  * in fp32 up to the one rounding of each output.
  *   activation  muon_activation, plus MUON_EXACT, MUON_FAST or neither.
  *   bias        fp32, one per row of b; NULL: none.
- *   residual    m x n, bf16 or fp32; NULL: none.
+ *   residual    m x n, bf16 or fp32; NULL: none.  It must not overlap y: a sum in
+ *               place is refused (MUON_ERR_INVALID_ARG).
  *   z           m x n, kept for the backward pass, of y's type, bf16 beside an
  *               8-bit result; NULL: not kept.
  *   y or y8     exactly one: bf16 or fp32, or (y NULL) an 8-bit tensor with

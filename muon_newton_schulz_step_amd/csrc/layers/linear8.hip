@@ -16,8 +16,8 @@ constexpr int kOut8 = 2;
 // x 528, 1024 x 4096, those columns 1% of all), an MLP's result by 2.4e-3 to 3.7e-3
 // and, of 200 rows of 128, 6.2e-3 where with exact products its rounding to bf16 leaves
 // 1.7e-3.  So 8-bit results come from exact products unless their caller chose speed
-// (fast): the up projection of an MLP with z kept takes 58 us instead of 43 (4096 x
-// 5120 x 1280) and 1705 instead of 979 (16384 x 16384 x 4096).
+// (fast): the up projection of an MLP with z kept takes 59 us instead of 44 (4096 x
+// 5120 x 1280) and 1722 instead of 1004 (16384 x 16384 x 4096).
 //
 // A plain product in 8 bits, without bias, activation, residual and z, is muon_matmul8's
 // with its result rounded once more, cut as that is, but where exact products cost

@@ -13,7 +13,8 @@
 // length by 1.5e-5 of the result's norm, 1/110 of what rounding it to bf16 does
 // (1.7e-3).  A result in fp32 keeps more than that, so it comes from bf16 MFMAs
 // at half the rate, to whose operands the values are converted exactly
-// (EXACT; 1e-7 of the norm).
+// (EXACT; 1e-7 of the norm); and so does one that an epilogue rounds to 8 bits
+// (linear8.hip).
 //
 // Two kernels:
 //   tiles   both operands through LDS, for many rows of a: bound by the MFMAs;
@@ -22,7 +23,8 @@
 // asked for, and act(z) + residual in bf16, fp32 or 8 bits.  What that costs a product
 // of 16384 x 16384 x 4096 (815 us on the same card): bias 15 us, squared ReLU 20, GELU
 // 110, a bf16 residual 90 (512 MB), an 8-bit result 58, and all of GELU, z kept and 8
-// bits 180; one of 4096 x 5120 x 1280 (38 us): 1, 2, 5, 6, 2 and 11.
+// bits 180; one of 4096 x 5120 x 1280 (38 us): 1, 2, 5, 6, 2 and 11 (products of the
+// 8-bit instruction in all).
 #pragma once
 
 #include "muon_gemm.h"
@@ -194,7 +196,7 @@ __device__ __forceinline__ void epilogue4(const Linear8Args& g, int m, int n, f3
 //   256 x 256 tiles on 8 waves, inputs in the caches: 8192 x 4096 x 4096 103 to
 //   110 us by box (2.5 to 2.67 PFLOP/s), 16384 x 16384 x 4096 788 to 798 us (2.75
 //   to 2.80), to fp32 216 and 1766 us (1.25).  They take all 256 registers and
-//   spill 8 (28 bytes a lane; to fp32 2).
+//   spill 5 (24 bytes a lane; exact ones 2, with an epilogue 6 to 8).
 //   A library's product with one scale per tensor runs at 2.72 to 2.80.  At the
 //   larger size the MFMAs are busy 70% of the cycles and the chip runs at 1.68
 //   GHz: it is bound by power.  Without the stores of y it would take 752 us.

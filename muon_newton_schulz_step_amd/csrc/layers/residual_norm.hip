@@ -15,20 +15,22 @@
 // lanes of a row in fp32 were 1.1 to 1.7 times as far off (4096 x 1280 by 1.9 against
 // 1.1 times 2^-24 sqrt(terms)) for 0 to 3% less time (16384 columns -8 to 9%); with
 // every term in fp64 it is off by 1.0 and costs up to 14% (16384 x 1280 fp32, bf16
-// branch: 104, 105 and 118 us).
+// branch: 104, 105 and 118 us, before rh, d and bh were made zeros past the last column,
+// which costs 2 us more there).
 //
 // Both passes read each element once and are bound by HBM:
-//   16384 x 1280 fp32, bf16 branch, gate and scale, to 8 bits 46 us (5.0 TB/s; a copy
-//   runs at 5.2); 8192 x 4096 bf16 with everything 57.5 us (4.7); backward 103 us
-//   (4.6) and 6 for the sums' reduction, 4096 x 8192 102, and of the RMS norm and
-//   residual sum alone 55 us (8192 x 4096) for both launches.
+//   16384 x 1280 fp32, bf16 branch, gate and scale, to 8 bits 46 to 48 us (4.9 TB/s; a
+//   copy runs at 5.2); 8192 x 4096 bf16 with everything 57 to 60 us (4.6); backward 96 to
+//   98 us (4.8) and 6 for the sums' reduction, 4096 x 8192 107 and 8, and of the RMS norm
+//   and residual sum alone 55 and 5 us (8192 x 4096).
 // As in layer norm a team of waves holds a row in registers, 8 consecutive columns
 // per lane (a chunk: 512 columns per wave), stays for many rows, and has its next row
-// on its way.  One chunk to a lane up to 8192 columns: with two or three the vectors
-// and sums left room for half the waves (1280 columns forward 61 us instead of 55,
-// backward 118 instead of 82, 4096 columns backward 182 instead of 105).  Where rows
-// are short of whole chunks (640, 1280) and both norms are there, the vector unit
-// bounds: 16384 x 1280 bf16 49 us forward, 75 backward (floors 32 and 57).
+// on its way.  One chunk to a lane up to 8192 columns, in the backward pass up to 4096:
+// with two or three the vectors and sums left room for half the waves (1280 columns
+// forward 61 us instead of 55, backward 118 instead of 82, 4096 columns backward 182
+// instead of 105).  Where rows are short of whole chunks (640, 1280) and both norms are
+// there, the vector unit bounds: 16384 x 1280 bf16 with everything 55 us forward, 91 and 5
+// backward (floors 32 and 57).
 #include "muon_block.h"
 #include "norm_device.h"
 

@@ -329,7 +329,8 @@ def linear8(a, b, bias=None, *, activation=None, residual=None, keep: bool = Fal
     ``activation`` None, "relu", "relu2" (squared), "gelu", "gelu_tanh" or
     "silu".  ``keep`` returns (y, z) with z = a b^T + bias for linear8_backward, in
     y's dtype (bf16 beside a Tensor8).  ``out`` may be given: a matrix in bf16 or fp32,
-    which may have a row stride, or a Tensor8.
+    which may have a row stride, or a Tensor8; none that overlaps ``residual`` or another
+    operand.
     Everything is fp32 up to the one rounding of each result.  Products are exact, but
     for bf16 results of many rows, which are those of matmul8 and cut far below their
     rounding, and for plain ones in 8 bits (without bias, activation, residual and

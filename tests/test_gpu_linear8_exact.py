@@ -149,3 +149,33 @@ def test_fast_by_choice(m, n, k, tile):
     assert np.array_equal(to64(got.data.float())[:, :n], q)
     with pytest.raises(ValueError):
         mn.linear8(a, b, out_dtype=FP32, exact=False)
+
+
+@pytest.mark.parametrize("m", [7, 90, 600])
+def test_operands_that_are_not_finite(m):
+    """A NaN in a row of a, or of b, is in that row, or column, of every result and in no
+    other place."""
+    announce("linear8: NaN in an operand", m)
+    n, k = 300, 1300
+    av, bv = whole(m, k, seed=1), whole(n, k, seed=2)
+    ref_a, ref_b = mn.quantize8(av), mn.quantize8(bv)
+    av[3, 700], bv[200, 64] = float("nan"), float("inf")
+    a, b = mn.quantize8(av), mn.quantize8(bv)
+    keep = torch.ones(m, n, dtype=torch.bool, device=DEV)
+    keep[3], keep[:, 200] = False, False
+    for out in (BF16, FP32, E4M3):
+        for exact in (None, True, False):
+            if out == FP32 and exact is False:
+                continue
+            y, z = mn.linear8(a, b, activation="silu", keep=True, out_dtype=out, exact=exact)
+            ref, zref = mn.linear8(ref_a, ref_b, activation="silu", keep=True, out_dtype=out, exact=exact)
+            assert torch.isnan(z[~keep]).all() and torch.equal(z[keep], zref[keep])
+            if out != E4M3:
+                assert torch.isnan(y[~keep]).all() and torch.equal(y[keep], ref[keep])
+                continue
+            assert torch.isnan(y.dequantize()[~keep]).all()
+            rows = keep.any(1)
+            blocks = [0, 2]                                   # of the column that is not finite: the second
+            assert torch.equal(y.scale[rows][:, blocks], ref.scale[rows][:, blocks])
+            for c in (slice(0, 128), slice(256, 300)):
+                assert torch.equal(y.data.view(torch.uint8)[rows][:, c], ref.data.view(torch.uint8)[rows][:, c])
